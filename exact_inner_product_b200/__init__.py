@@ -37,8 +37,10 @@ TT_NORM_STORE = 0
 TT_NORM_FUSED = 1
 TT_MAX_D = 512
 TT_MAX_K = 2048
+TT_MAX_WIDTH = 16384
 
-KIND_NAMES = ("normalize", "cast", "stream", "tensor", "select", "aux", "softmax", "estimate")
+KIND_NAMES = ("normalize", "cast", "stream", "tensor", "select", "aux", "softmax", "estimate",
+              "rownorm")
 TT_NUM_KINDS = len(KIND_NAMES)
 
 if not os.path.exists(LIB_PATH):
@@ -96,6 +98,12 @@ _sig("tt_inbatch_softmax_workspace", ctypes.c_int, [_i32, _i32, _i32, _i32, ctyp
 _sig("tt_inbatch_softmax", ctypes.c_int, [_vp, _vp, ctypes.c_int, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _vp,
                                           _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp])
 _sig("tt_inbatch_softmax_check", ctypes.c_int, [_vp, _vp])
+_sig("tt_layernorm", ctypes.c_int, [_vp, ctypes.c_int, _i64, _i32, _vp, _vp, ctypes.c_int, ctypes.c_float, _vp, _vp,
+                                    _vp, _vp])
+_sig("tt_layernorm_grad_workspace", ctypes.c_int, [_i64, _i32, ctypes.POINTER(ctypes.c_size_t)])
+_sig("tt_layernorm_grad", ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i32, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
+                                         _vp, ctypes.c_size_t, _vp])
+_sig("tt_normalize_grad", ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _i64, _i32, _vp, _vp])
 _sig("tt_free", None, [_vp])
 _sig("tt_launch_count", _i64, [])
 _sig("tt_profile_begin", ctypes.c_int, [])
@@ -110,6 +118,7 @@ EXPORTED = ("tt_normalize_candidates", "tt_quantize_candidates", "tt_index_wrap"
             "tt_index_check", "tt_score_topk_host",
             "tt_score_topk_noalloc", "tt_merge_topk", "tt_score_topk_ranges", "tt_score_topk_types",
             "tt_inbatch_softmax_workspace", "tt_inbatch_softmax", "tt_inbatch_softmax_check",
+            "tt_layernorm", "tt_layernorm_grad_workspace", "tt_layernorm_grad", "tt_normalize_grad",
             "tt_last_stats", "tt_plan", "tt_free", "tt_launch_count", "tt_profile_begin",
             "tt_profile_end", "tt_profile_launches", "tt_status_string", "tt_last_error", "tt_version")
 
@@ -412,6 +421,112 @@ def tt_inbatch_softmax(users: torch.Tensor, items: torch.Tensor, tau: float = 1.
     if check:
         _check(_lib.tt_inbatch_softmax_check(_ptr(workspace), _stream(stream)), "tt_inbatch_softmax")
     return lse, loss, mean
+
+
+def _check_float(name: str, t: torch.Tensor, shape=None, dtypes=(torch.float32, torch.bfloat16), device=None):
+    """A contiguous CUDA tensor of one of ``dtypes`` (and of ``shape``, on ``device``)."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+        want = "" if shape is None else f" of shape {tuple(shape)}"
+        raise ValueError(f"{name} must be a contiguous CUDA tensor{want}, got {tuple(t.shape)} on {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _workspace(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _check_float("workspace", workspace, dtypes=(torch.uint8,), device=device)
+    return workspace
+
+
+def tt_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                 eps: float = 1e-5, out: tuple | None = None, stream=None):
+    """Layer norm of the rows of ``x`` [n, d] (``tt_layernorm``), float32 or
+    bfloat16. ``weight`` and ``bias``: [d], of one dtype, or None. Returns
+    ``(y [n, d], mean [n], rstd [n])``, y in x's dtype and the statistics in
+    float32; ``out`` gives the three tensors to write."""
+    if x.dim() != 2:
+        raise ValueError("x must be [n, d]")
+    _check_float("x", x)
+    n, d = x.shape
+    dev = x.device
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check_float(name, t, (d,), device=dev)
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have one dtype")
+    if out is None:
+        out = (torch.empty_like(x), torch.empty(n, dtype=torch.float32, device=dev),
+               torch.empty(n, dtype=torch.float32, device=dev))
+    else:
+        _check_float("out y", out[0], (n, d), (x.dtype,), dev)
+        _check_float("out mean", out[1], (n,), (torch.float32,), dev)
+        _check_float("out rstd", out[2], (n,), (torch.float32,), dev)
+    y, mean, rstd = out
+    p = weight if weight is not None else bias
+    _check(_lib.tt_layernorm(_ptr(x), _dtype(x), n, d, _ptr(weight), _ptr(bias), TT_F32 if p is None else _dtype(p),
+                             float(eps), _ptr(y), _ptr(mean), _ptr(rstd), _stream(stream)), "tt_layernorm")
+    return y, mean, rstd
+
+
+def tt_layernorm_grad_workspace(n: int, d: int) -> int:
+    """Bytes of device workspace ``tt_layernorm_grad`` needs for these sizes."""
+    need = ctypes.c_size_t(0)
+    _check(_lib.tt_layernorm_grad_workspace(int(n), int(d), ctypes.byref(need)), "tt_layernorm_grad_workspace")
+    return int(need.value)
+
+
+def tt_layernorm_grad(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                      rstd: torch.Tensor, out: tuple | None = None, workspace: torch.Tensor | None = None,
+                      stream=None):
+    """The gradient of ``tt_layernorm`` (``tt_layernorm_grad``). ``mean`` and
+    ``rstd`` are the forward call's. Returns ``(grad_x [n, d], grad_weight [d],
+    grad_bias [d])``, the first in x's dtype, the others in float32. ``out``
+    gives the three tensors to write; one that is None there is not computed."""
+    if x.dim() != 2:
+        raise ValueError("x must be [n, d]")
+    _check_float("x", x)
+    n, d = x.shape
+    dev = x.device
+    _check_float("grad_y", grad_y, (n, d), (x.dtype,), dev)
+    if weight is not None:
+        _check_float("weight", weight, (d,), device=dev)
+    _check_float("mean", mean, (n,), (torch.float32,), dev)
+    _check_float("rstd", rstd, (n,), (torch.float32,), dev)
+    if out is None:
+        out = (torch.empty_like(x), torch.empty(d, dtype=torch.float32, device=dev),
+               torch.empty(d, dtype=torch.float32, device=dev))
+    else:
+        for name, t, shape, dt in (("out grad_x", out[0], (n, d), x.dtype), ("out grad_weight", out[1], (d,), torch.float32),
+                                   ("out grad_bias", out[2], (d,), torch.float32)):
+            if t is not None:
+                _check_float(name, t, shape, (dt,), dev)
+    workspace = _workspace(workspace, tt_layernorm_grad_workspace(n, d) if workspace is None else 0, dev)
+    _check(_lib.tt_layernorm_grad(_ptr(grad_y), _ptr(x), _dtype(x), n, d, _ptr(weight),
+                                  TT_F32 if weight is None else _dtype(weight), _ptr(mean), _ptr(rstd), _ptr(out[0]),
+                                  _ptr(out[1]), _ptr(out[2]), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "tt_layernorm_grad")
+    return tuple(out)
+
+
+def tt_normalize_grad(grad_y: torch.Tensor, x: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+    """The gradient of the row-wise L2 normalisation (``tt_normalize_grad``):
+    ``x`` [n, d] are the rows before it, ``grad_y`` [n, d] the gradient of the
+    normalised rows. Returns grad_x in x's dtype."""
+    if x.dim() != 2:
+        raise ValueError("x must be [n, d]")
+    _check_float("x", x)
+    _check_float("grad_y", grad_y, x.shape, device=x.device)
+    n, d = x.shape
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check_float("out", out, x.shape, (x.dtype,), x.device)
+    _check(_lib.tt_normalize_grad(_ptr(grad_y), _dtype(grad_y), _ptr(x), _dtype(x), n, d, _ptr(out), _stream(stream)),
+           "tt_normalize_grad")
+    return out
 
 
 def _check_queries(index: Index, queries: torch.Tensor, exclude):

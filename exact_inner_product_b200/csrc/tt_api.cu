@@ -65,7 +65,7 @@ namespace tt {
 // ---------------------------------------------------------------------------
 static thread_local char g_last_error[256] = {0};
 
-static tt_status cuda_fail(cudaError_t e, const char* what) {
+tt_status cuda_fail(cudaError_t e, const char* what) {
     snprintf(g_last_error, sizeof g_last_error, "%s: %s", what, cudaGetErrorString(e));
     return e == cudaErrorMemoryAllocation ? TT_ERR_NO_MEMORY : TT_ERR_CUDA;
 }
@@ -191,9 +191,9 @@ static bool tile_tensor_map(int dtype, const void* base, int64_t rows, int d, in
 // ---------------------------------------------------------------------------
 // validation helpers
 // ---------------------------------------------------------------------------
-static bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-static bool valid_dtype(int dt) { return dt == TT_F32 || dt == TT_BF16; }
+bool valid_dtype(int dt) { return dt == TT_F32 || dt == TT_BF16; }
 static bool valid_index_dtype(int dt) { return valid_dtype(dt) || dt == TT_I8; }
 
 static tt_status check_d(int32_t d) {
@@ -203,7 +203,7 @@ static tt_status check_d(int32_t d) {
 }
 
 // The pointer must be device (or managed) memory of the current device.
-static tt_status check_device_ptr(const void* p, const char* what) {
+tt_status check_device_ptr(const void* p, const char* what) {
     if (p == nullptr) return TT_OK;
     cudaPointerAttributes attr;
     cudaError_t e = cudaPointerGetAttributes(&attr, p);
@@ -226,7 +226,7 @@ static tt_status check_device_ptr(const void* p, const char* what) {
     return TT_OK;
 }
 
-static int sm_count_current() {
+int sm_count_current() {
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

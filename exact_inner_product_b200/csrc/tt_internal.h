@@ -46,6 +46,13 @@ struct PassArgs {
     int defer;                 // streaming pass right after the one-sample estimate (its thresholds)
 };
 
+// Host helpers of the C ABI (tt_api.cu), shared by its source files.
+tt_status cuda_fail(cudaError_t e, const char* what);  // records the message; TT_ERR_CUDA or TT_ERR_NO_MEMORY
+bool aligned(const void* p, uintptr_t a);
+bool valid_dtype(int dt);  // TT_F32 or TT_BF16
+tt_status check_device_ptr(const void* p, const char* what);
+int sm_count_current();
+
 // Launch `kernel` with programmatic stream serialization: it may start while
 // the stream's previous kernel still runs (the kernel then orders its memory
 // accesses with pdl_wait(), see tt_device.cuh).
@@ -251,5 +258,16 @@ cudaError_t launch_offset_ids(int32_t* ids, int64_t count, int64_t offset, cudaS
 int tensor_pass_smem_bytes(int d, int nq_tile, int esize);
 int tensor_pass_max_nq(int d, int esize);
 int tensor_pair_smem_bytes(int d, int esize);  // -1 when d does not fit (esize: 2 bf16, 1 int8)
+
+// Layer norm and the gradients of the row norms (k_rownorm.cu). `part` holds
+// layernorm_grad_bytes; w, bias, mean, rstd (forward) and dx, dw, db may be null.
+size_t layernorm_grad_bytes(int64_t n, int d, int sm_count);
+cudaError_t launch_layernorm(const void* x, int x_dtype, int64_t n, int d, const void* w, const void* bias,
+                             int w_dtype, float eps, void* y, float* mean, float* rstd, cudaStream_t s, int sm_count);
+cudaError_t launch_layernorm_grad(const void* dy, const void* x, int x_dtype, int64_t n, int d, const void* w,
+                                  int w_dtype, const float* mean, const float* rstd, void* dx, float* dw, float* db,
+                                  float* part, cudaStream_t s, int sm_count);
+cudaError_t launch_normalize_grad(const void* dy, int dy_dtype, const void* x, int x_dtype, int64_t n, int d, void* dx,
+                                  cudaStream_t s, int sm_count);
 
 }  // namespace tt

@@ -1,0 +1,165 @@
+// tt_train_api.cu - the C ABI of the training-step operators: argument
+// validation and launches. Conventions and errors as in tt_api.cu.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <stdio.h>
+
+#include "../../include/tt.h"
+#include "tt_internal.h"
+
+namespace tt {
+namespace {
+
+size_t elem_bytes(int dtype) { return dtype == TT_F32 ? 4 : 2; }
+
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    if (a == nullptr || b == nullptr || a_bytes == 0 || b_bytes == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
+// The buffers of a call. Outputs may overlap nothing; inputs may overlap
+// inputs. Null buffers are skipped.
+struct Buffers {
+    struct One {
+        const void* p;
+        size_t bytes;
+        const char* name;
+        bool out;
+    };
+    One list[20];
+    int count = 0;
+    void add(const void* p, size_t bytes, const char* name, bool out) {
+        if (p != nullptr) list[count++] = {p, bytes, name, out};
+    }
+    void in(const void* p, size_t bytes, const char* name) { add(p, bytes, name, false); }
+    void out(const void* p, size_t bytes, const char* name) { add(p, bytes, name, true); }
+    // host-side check, then the device pointers
+    tt_status check() const {
+        for (int i = 0; i < count; ++i)
+            for (int j = 0; j < i; ++j)
+                if ((list[i].out || list[j].out) && overlap(list[i].p, list[i].bytes, list[j].p, list[j].bytes)) {
+                    char msg[160];
+                    snprintf(msg, sizeof msg, "%s overlaps %s", list[i].name, list[j].name);
+                    set_last_error_message(msg);
+                    return TT_ERR_INVALID_ARG;
+                }
+        for (int i = 0; i < count; ++i) {
+            const tt_status st = check_device_ptr(list[i].p, list[i].name);
+            if (st != TT_OK) return st;
+        }
+        return TT_OK;
+    }
+};
+
+tt_status check_workspace(const void* workspace, size_t have, size_t need) {
+    if (workspace == nullptr || !aligned(workspace, 256)) return TT_ERR_INVALID_ARG;
+    if (have < need) {
+        char msg[96];
+        snprintf(msg, sizeof msg, "workspace of %zu bytes, need %zu", have, need);
+        set_last_error_message(msg);
+        return TT_ERR_INVALID_ARG;
+    }
+    return TT_OK;
+}
+
+tt_status check_rows(int64_t n, int32_t d) {
+    if (n < 0 || d <= 0) return TT_ERR_INVALID_ARG;
+    if (n > TT_MAX_N || d > TT_MAX_WIDTH) return TT_ERR_UNSUPPORTED;
+    return TT_OK;
+}
+
+}  // namespace
+}  // namespace tt
+
+using namespace tt;
+
+extern "C" {
+
+tt_status tt_layernorm(const void* x, tt_dtype dtype, int64_t n, int32_t d, const void* w, const void* bias,
+                       tt_dtype w_dtype, float eps, void* y, float* mean, float* rstd, void* stream) {
+    tt_status st = check_rows(n, d);
+    if (st != TT_OK) return st;
+    if (!valid_dtype(dtype) || !valid_dtype(w_dtype)) return TT_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !isfinite(eps)) return TT_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(y, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return TT_ERR_INVALID_ARG;
+    if (n == 0) return TT_OK;
+    if (x == nullptr || y == nullptr) return TT_ERR_INVALID_ARG;
+    const size_t row_bytes = (size_t)n * d * elem_bytes(dtype), w_bytes = d * elem_bytes(w_dtype);
+    Buffers b;
+    b.in(x, row_bytes, "x");
+    b.in(w, w_bytes, "w");
+    b.in(bias, w_bytes, "bias");
+    b.out(y, row_bytes, "y");
+    b.out(mean, n * sizeof(float), "mean");
+    b.out(rstd, n * sizeof(float), "rstd");
+    if ((st = b.check()) != TT_OK) return st;
+    const cudaError_t e = launch_layernorm(x, dtype, n, d, w, bias, w_dtype, eps, y, mean, rstd,
+                                           static_cast<cudaStream_t>(stream), sm_count_current());
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "layer norm");
+}
+
+tt_status tt_layernorm_grad_workspace(int64_t n, int32_t d, size_t* bytes) {
+    if (bytes == nullptr) return TT_ERR_INVALID_ARG;
+    const tt_status st = check_rows(n, d);
+    if (st != TT_OK) return st;
+    *bytes = layernorm_grad_bytes(n, d, sm_count_current());
+    return TT_OK;
+}
+
+tt_status tt_layernorm_grad(const void* grad_y, const void* x, tt_dtype dtype, int64_t n, int32_t d, const void* w,
+                            tt_dtype w_dtype, const float* mean, const float* rstd, void* grad_x, float* grad_w,
+                            float* grad_bias, void* workspace, size_t workspace_bytes, void* stream) {
+    tt_status st = check_rows(n, d);
+    if (st != TT_OK) return st;
+    if (!valid_dtype(dtype) || !valid_dtype(w_dtype)) return TT_ERR_INVALID_ARG;
+    if (!aligned(grad_y, 16) || !aligned(x, 16) || !aligned(grad_x, 16) || !aligned(w, 16) || !aligned(mean, 4) ||
+        !aligned(rstd, 4) || !aligned(grad_w, 4) || !aligned(grad_bias, 4))
+        return TT_ERR_INVALID_ARG;
+    if (n > 0 && (grad_y == nullptr || x == nullptr || mean == nullptr || rstd == nullptr)) return TT_ERR_INVALID_ARG;
+    const int sms = sm_count_current();
+    const size_t need = layernorm_grad_bytes(n, d, sms);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != TT_OK) return st;
+    const size_t row_bytes = (size_t)n * d * elem_bytes(dtype);
+    Buffers b;
+    b.in(grad_y, row_bytes, "grad_y");
+    b.in(x, row_bytes, "x");
+    b.in(w, d * elem_bytes(w_dtype), "w");
+    b.in(mean, n * sizeof(float), "mean");
+    b.in(rstd, n * sizeof(float), "rstd");
+    b.out(grad_x, row_bytes, "grad_x");
+    b.out(grad_w, d * sizeof(float), "grad_w");
+    b.out(grad_bias, d * sizeof(float), "grad_bias");
+    b.out(workspace, need, "workspace");
+    if ((st = b.check()) != TT_OK) return st;
+    const cudaError_t e =
+        launch_layernorm_grad(grad_y, x, dtype, n, d, w, w_dtype, mean, rstd, grad_x, grad_w, grad_bias,
+                              static_cast<float*>(workspace), static_cast<cudaStream_t>(stream), sms);
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "layer norm gradient");
+}
+
+tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x, tt_dtype dtype, int64_t n, int32_t d,
+                            void* grad_x, void* stream) {
+    if (n < 0 || d <= 0) return TT_ERR_INVALID_ARG;
+    if (n > TT_MAX_N || d % 16 != 0 || d > TT_MAX_D) return TT_ERR_UNSUPPORTED;
+    if (!valid_dtype(dtype) || !valid_dtype(g_dtype)) return TT_ERR_INVALID_ARG;
+    if (!aligned(grad_y, 16) || !aligned(x, 16) || !aligned(grad_x, 16)) return TT_ERR_INVALID_ARG;
+    if (n == 0) return TT_OK;
+    if (grad_y == nullptr || x == nullptr || grad_x == nullptr) return TT_ERR_INVALID_ARG;
+    const size_t elems = (size_t)n * d;
+    Buffers b;
+    b.in(grad_y, elems * elem_bytes(g_dtype), "grad_y");
+    b.in(x, elems * elem_bytes(dtype), "x");
+    b.out(grad_x, elems * elem_bytes(dtype), "grad_x");
+    tt_status st = b.check();
+    if (st != TT_OK) return st;
+    const cudaError_t e = launch_normalize_grad(grad_y, g_dtype, x, dtype, n, d, grad_x,
+                                                static_cast<cudaStream_t>(stream), sm_count_current());
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "normalisation gradient");
+}
+
+}  // extern "C"

@@ -71,6 +71,7 @@ typedef enum tt_norm_mode {
 #define TT_MAX_PARTS 64     /* shards merged by one tt_merge_topk call; result sets of one call */
 #define TT_MAX_SET_LISTS (1 << 24) /* tt_score_topk_types: n_sets * b at most this */
 #define TT_MAX_N 2147483647 /* candidate ids are int32: n < 2^31 */
+#define TT_MAX_WIDTH 16384  /* layer norm and embedding rows: 1 <= d <= 16384, any d */
 
 /* Opaque handle describing a prepared corpus. Owned by the library; release
  * with tt_free. It refers to, but does not own, the caller's corpus buffers,
@@ -413,6 +414,77 @@ TT_API tt_status tt_inbatch_softmax(const void* users, const void* items, tt_dty
  * and report TT_OK or TT_ERR_TIMEOUT. */
 TT_API tt_status tt_inbatch_softmax_check(const void* workspace, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The training step around the loss: what lies between the embedding tables
+ * and the vectors that tt_inbatch_softmax takes, and the gradients on the way
+ * back. (The pages give the towers, recsys_two_tower_model.py, and the loss;
+ * the gradients they leave to automatic differentiation.)
+ *
+ * All of these calls are asynchronous on `stream`, allocate nothing, wait for
+ * nothing on the host, and can be captured in a CUDA graph. Outputs must not
+ * overlap inputs or one another (TT_ERR_INVALID_ARG) unless the call says so.
+ * Where a call takes a workspace, it is device memory of at least the bytes
+ * that the matching _workspace call returns, 256-byte aligned, owned by the
+ * caller, its contents meaningless before and after, and not shared with
+ * another call in flight (two graphs that may run at once need one each).
+ * Results do not depend on scheduling: the same call on the same GPU model
+ * gives the same bits.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * tt_layernorm - layer norm of every row.
+ *
+ *   mean = sum_i x_i / d,  rstd = 1 / sqrt(sum_i (x_i - mean)^2 / d + eps)
+ *   y_i  = (x_i - mean) rstd w_i + bias_i       (fp32 arithmetic)
+ *
+ * x, y        device [n, d] dtype (TT_F32 or TT_BF16); y is rounded to dtype
+ * n           0 <= n < 2^31 (n = 0: nothing to do)
+ * d           1 <= d <= TT_MAX_WIDTH, any value (multiples of 8 are fastest)
+ * w, bias     device [d] w_dtype (TT_F32 or TT_BF16), 16-byte aligned, either
+ *             may be NULL (1 and 0)
+ * eps         finite, >= 0 (with 0, a constant row gives 0 * inf = NaN)
+ * mean, rstd  device f32 [n], either may be NULL: kept for the gradient
+ */
+TT_API tt_status tt_layernorm(const void* x, tt_dtype dtype, int64_t n, int32_t d, const void* w, const void* bias,
+                              tt_dtype w_dtype, float eps, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * tt_layernorm_grad - the gradient of tt_layernorm.
+ *
+ *   xhat = (x - mean) rstd,  g = grad_y w
+ *   grad_x    = rstd (g - sum_i g_i / d - xhat sum_i(g_i xhat_i) / d)
+ *   grad_w    = sum over rows of grad_y xhat
+ *   grad_bias = sum over rows of grad_y
+ *
+ * grad_y, x   device [n, d] dtype; grad_x device [n, d] dtype or NULL
+ * w           device [d] w_dtype or NULL
+ * mean, rstd  device f32 [n], as tt_layernorm wrote them
+ * grad_w,     device f32 [d], either may be NULL. Summed in fp32 in an order
+ * grad_bias   that the sizes fix. Zero for n = 0.
+ * workspace   tt_layernorm_grad_workspace bytes
+ */
+TT_API tt_status tt_layernorm_grad_workspace(int64_t n, int32_t d, size_t* bytes);
+TT_API tt_status tt_layernorm_grad(const void* grad_y, const void* x, tt_dtype dtype, int64_t n, int32_t d,
+                                   const void* w, tt_dtype w_dtype, const float* mean, const float* rstd,
+                                   void* grad_x, float* grad_w, float* grad_bias, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * tt_normalize_grad - the gradient of tt_normalize_candidates (TT_NORM_STORE)
+ * with respect to its input rows.
+ *
+ *   norm = sqrt(max(sum_i x_i^2, 1e-12)),  y = x / norm
+ *   grad_x = (grad_y - y sum_i(y_i grad_y_i)) / norm
+ *   (where sum_i x_i^2 < 1e-12 norm is a constant: grad_x = grad_y / norm)
+ *
+ * grad_y  device [n, d] g_dtype (TT_F32 or TT_BF16)
+ * x       device [n, d] dtype: the rows before the normalisation
+ * grad_x  device [n, d] dtype
+ * n, d    as tt_normalize_candidates
+ */
+TT_API tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x, tt_dtype dtype, int64_t n,
+                                   int32_t d, void* grad_x, void* stream);
+
 /* Release a handle. Its work memory returns to a per-device pool that later
  * handles reuse (it is not returned to CUDA before the process exits); a
  * later user's stream first waits for the work this handle had enqueued, so
@@ -472,7 +544,8 @@ TT_API tt_status tt_score_topk_noalloc(const void* rows, tt_dtype dtype, int64_t
 #define TT_KIND_AUX 5
 #define TT_KIND_SOFTMAX 6  /* tt_inbatch_softmax */
 #define TT_KIND_ESTIMATE 7 /* the sampled threshold estimate of a small batch */
-#define TT_NUM_KINDS 8
+#define TT_KIND_ROWNORM 8  /* layer norm, and the gradients of the row norms */
+#define TT_NUM_KINDS 9
 
 /* Total kernels this library has launched in the process. */
 TT_API int64_t tt_launch_count(void);

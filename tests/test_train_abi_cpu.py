@@ -1,0 +1,58 @@
+"""The training-step entry points on a machine without a GPU: arguments are
+refused on the host, before any device call. No compute call is made here."""
+import ctypes
+
+import pytest
+
+tt = pytest.importorskip("exact_inner_product_b200")
+
+INV, UNS = tt.TT_ERR_INVALID_ARG, tt.TT_ERR_UNSUPPORTED
+P = [ctypes.c_void_p(0x1000000 * (i + 1)) for i in range(12)]  # never dereferenced
+ODD = ctypes.c_void_p(0x1000002)
+
+
+def test_layernorm_arguments():
+    def call(x=P[0], dt=0, n=4, d=64, w=P[1], bias=P[2], wdt=0, eps=1e-5, y=P[3], mean=P[4], rstd=P[5]):
+        return tt._lib.tt_layernorm(x, dt, n, d, w, bias, wdt, eps, y, mean, rstd, None)
+
+    assert call(n=-1) == INV and call(d=0) == INV and call(d=-5) == INV
+    assert call(d=tt.TT_MAX_WIDTH + 1) == UNS and call(n=1 << 31) == UNS
+    assert call(dt=tt.TT_I8) == INV and call(wdt=7) == INV
+    assert call(eps=-1.0) == INV and call(eps=float("nan")) == INV and call(eps=float("inf")) == INV
+    assert call(x=None) == INV and call(y=None) == INV
+    assert call(x=ODD) == INV and call(y=ODD) == INV and call(w=ODD) == INV and call(mean=ODD) == INV
+    assert call(y=P[0]) == INV                                   # in place
+    assert call(mean=P[5]) == INV                                # mean is rstd
+    assert call(rstd=ctypes.c_void_p(P[0].value + 16)) == INV    # inside x
+    assert call(n=0, x=None, y=None) == tt.TT_OK
+
+
+def test_layernorm_grad_arguments():
+    size = ctypes.c_size_t(0)
+    assert tt._lib.tt_layernorm_grad_workspace(4, 64, None) == INV
+    assert tt._lib.tt_layernorm_grad_workspace(-1, 64, ctypes.byref(size)) == INV
+    assert tt._lib.tt_layernorm_grad_workspace(4, 20000, ctypes.byref(size)) == UNS
+    assert tt._lib.tt_layernorm_grad_workspace(4, 64, ctypes.byref(size)) == tt.TT_OK
+    need = size.value
+    assert need >= 2 * 64 * 4
+
+    def call(dy=P[0], x=P[1], dt=0, n=4, d=64, w=P[2], wdt=0, mean=P[3], rstd=P[4], gx=P[5], gw=P[6], gb=P[7], ws=P[8],
+             size=need):
+        return tt._lib.tt_layernorm_grad(dy, x, dt, n, d, w, wdt, mean, rstd, gx, gw, gb, ws, size, None)
+
+    assert call(n=-1) == INV and call(d=0) == INV and call(d=20000) == UNS
+    assert call(dt=9) == INV and call(wdt=tt.TT_I8) == INV
+    assert call(dy=None) == INV and call(x=None) == INV and call(mean=None) == INV and call(rstd=None) == INV
+    assert call(ws=None) == INV and call(ws=ODD) == INV and call(size=need - 1) == INV
+    assert call(gx=ODD) == INV and call(gx=P[1]) == INV and call(gx=P[0]) == INV and call(gw=P[7]) == INV
+
+
+def test_normalize_grad_arguments():
+    def call(dy=P[0], gdt=0, x=P[1], dt=0, n=4, d=64, gx=P[2]):
+        return tt._lib.tt_normalize_grad(dy, gdt, x, dt, n, d, gx, None)
+
+    assert call(n=-1) == INV and call(d=0) == INV and call(d=40) == UNS and call(d=528) == UNS and call(n=1 << 31) == UNS
+    assert call(dt=tt.TT_I8) == INV and call(gdt=5) == INV
+    assert call(dy=None) == INV and call(x=None) == INV and call(gx=None) == INV and call(gx=ODD) == INV
+    assert call(gx=P[0]) == INV and call(gx=P[1]) == INV
+    assert call(n=0, dy=None, x=None, gx=None) == tt.TT_OK
