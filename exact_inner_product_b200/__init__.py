@@ -40,7 +40,7 @@ TT_MAX_K = 2048
 TT_MAX_WIDTH = 16384
 
 KIND_NAMES = ("normalize", "cast", "stream", "tensor", "select", "aux", "softmax", "estimate",
-              "rownorm")
+              "rownorm", "clip")
 TT_NUM_KINDS = len(KIND_NAMES)
 
 if not os.path.exists(LIB_PATH):
@@ -104,6 +104,9 @@ _sig("tt_layernorm_grad_workspace", ctypes.c_int, [_i64, _i32, ctypes.POINTER(ct
 _sig("tt_layernorm_grad", ctypes.c_int, [_vp, _vp, ctypes.c_int, _i64, _i32, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
                                          _vp, ctypes.c_size_t, _vp])
 _sig("tt_normalize_grad", ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _i64, _i32, _vp, _vp])
+_sig("tt_clip_grad_norm_workspace", ctypes.c_int, [_i32, _vp, _vp, ctypes.POINTER(ctypes.c_size_t)])
+_sig("tt_grad_norm", ctypes.c_int, [_i32, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp])
+_sig("tt_clip_grad_norm", ctypes.c_int, [_i32, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, ctypes.c_size_t, _vp])
 _sig("tt_free", None, [_vp])
 _sig("tt_launch_count", _i64, [])
 _sig("tt_profile_begin", ctypes.c_int, [])
@@ -119,6 +122,7 @@ EXPORTED = ("tt_normalize_candidates", "tt_quantize_candidates", "tt_index_wrap"
             "tt_score_topk_noalloc", "tt_merge_topk", "tt_score_topk_ranges", "tt_score_topk_types",
             "tt_inbatch_softmax_workspace", "tt_inbatch_softmax", "tt_inbatch_softmax_check",
             "tt_layernorm", "tt_layernorm_grad_workspace", "tt_layernorm_grad", "tt_normalize_grad",
+            "tt_clip_grad_norm_workspace", "tt_grad_norm", "tt_clip_grad_norm",
             "tt_last_stats", "tt_plan", "tt_free", "tt_launch_count", "tt_profile_begin",
             "tt_profile_end", "tt_profile_launches", "tt_status_string", "tt_last_error", "tt_version")
 
@@ -527,6 +531,78 @@ def tt_normalize_grad(grad_y: torch.Tensor, x: torch.Tensor, out: torch.Tensor |
     _check(_lib.tt_normalize_grad(_ptr(grad_y), _dtype(grad_y), _ptr(x), _dtype(x), n, d, _ptr(out), _stream(stream)),
            "tt_normalize_grad")
     return out
+
+
+_ELEM = {torch.float32: TT_F32, torch.bfloat16: TT_BF16}
+
+
+def _tensor_list(name: str, tensors, like=None):
+    """Device pointers of contiguous float32/bfloat16 CUDA tensors, as a ctypes array."""
+    for i, t in enumerate(tensors):
+        if t.dtype not in _ELEM:
+            raise TypeError(f"{name}[{i}] must be float32 or bfloat16, got {t.dtype}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor")
+        if like is not None and (t.dtype != like[i].dtype or t.shape != like[i].shape):
+            raise ValueError(f"{name}[{i}] must have the dtype and shape of its gradient")
+    return (_vp * max(1, len(tensors)))(*[t.data_ptr() for t in tensors])
+
+
+def _norm_call(tensors, norm, workspace):
+    tensors = list(tensors)
+    count = len(tensors)
+    ptrs = _tensor_list("grads", tensors)
+    n = (_i64 * max(1, count))(*[t.numel() for t in tensors])
+    dtypes = (_i32 * max(1, count))(*[_ELEM[t.dtype] for t in tensors])
+    dev = tensors[0].device if count else torch.device("cuda", torch.cuda.current_device())
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+    else:
+        _check_float("norm", norm, (), (torch.float32,), dev)
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _check(_lib.tt_clip_grad_norm_workspace(count, n, dtypes, ctypes.byref(need)), "tt_clip_grad_norm_workspace")
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    else:
+        _check_float("workspace", workspace, dtypes=(torch.uint8,), device=dev)
+    return tensors, count, ptrs, n, dtypes, norm, workspace
+
+
+def tt_clip_grad_norm_workspace(grads) -> int:
+    """Bytes of device workspace ``tt_grad_norm`` and ``tt_clip_grad_norm`` need for these tensors."""
+    grads = list(grads)
+    need = ctypes.c_size_t(0)
+    n = (_i64 * max(1, len(grads)))(*[t.numel() for t in grads])
+    dtypes = (_i32 * max(1, len(grads)))(*[_dtype(t) for t in grads])
+    _check(_lib.tt_clip_grad_norm_workspace(len(grads), n, dtypes, ctypes.byref(need)), "tt_clip_grad_norm_workspace")
+    return int(need.value)
+
+
+def tt_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """The L2 norm of all elements of the tensors ``grads`` (float32 and
+    bfloat16 may be mixed), as a float32 scalar on the device (``tt_grad_norm``)."""
+    _, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace)
+    _check(_lib.tt_grad_norm(count, ptrs, n, dtypes, _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "tt_grad_norm")
+    return norm
+
+
+def tt_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """Scale the tensors ``grads`` so that their global L2 norm is at most
+    ``max_norm`` (``tt_clip_grad_norm``): in place, or into the tensors of
+    ``out``. Returns the norm before the scaling, a float32 scalar on the
+    device; nothing is read back to the host."""
+    grads, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace)
+    outs = None
+    if out is not None:
+        out = list(out)
+        if len(out) != count:
+            raise ValueError(f"out has {len(out)} tensors for {count} gradients")
+        outs = _tensor_list("out", out, like=grads)
+    _check(_lib.tt_clip_grad_norm(count, ptrs, n, dtypes, outs, float(max_norm), _ptr(norm), _ptr(workspace),
+                                  workspace.numel(), _stream(stream)), "tt_clip_grad_norm")
+    return norm
 
 
 def _check_queries(index: Index, queries: torch.Tensor, exclude):

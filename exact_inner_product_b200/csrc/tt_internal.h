@@ -270,4 +270,19 @@ cudaError_t launch_layernorm_grad(const void* dy, const void* x, int x_dtype, in
 cudaError_t launch_normalize_grad(const void* dy, int dy_dtype, const void* x, int x_dtype, int64_t n, int d, void* dx,
                                   cudaStream_t s, int sm_count);
 
+// Global norm and clipping of many tensors (k_clip.cu): host arrays of count
+// entries; tensor i holds n[i] < 2^42 elements, out[i] is in[i] or disjoint
+// from everything. `part` holds clip_workspace_bytes.
+constexpr int CLIP_MAX_TENSORS = 1000;  // per launch
+struct ClipList {
+    int count;
+    const void* const* in;
+    void* const* out;
+    const int64_t* n;
+    const int32_t* dtype;
+};
+size_t clip_workspace_bytes(const ClipList& l, int sm_count);
+cudaError_t launch_clip(const ClipList& l, bool scale, float max_norm, float* norm, double* part, cudaStream_t s,
+                        int sm_count);
+
 }  // namespace tt

@@ -5,6 +5,9 @@
 #include <math.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <stdlib.h>
+
+#include <algorithm>
 
 #include "../../include/tt.h"
 #include "tt_internal.h"
@@ -69,6 +72,79 @@ tt_status check_rows(int64_t n, int32_t d) {
     if (n < 0 || d <= 0) return TT_ERR_INVALID_ARG;
     if (n > TT_MAX_N || d > TT_MAX_WIDTH) return TT_ERR_UNSUPPORTED;
     return TT_OK;
+}
+
+tt_status check_clip_list(int32_t count, const int64_t* n, const int32_t* dtypes) {
+    if (count < 0 || (count > 0 && (n == nullptr || dtypes == nullptr))) return TT_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        if (!valid_dtype(dtypes[i]) || n[i] < 0) return TT_ERR_INVALID_ARG;
+        if (n[i] >= (int64_t)1 << 42) return TT_ERR_UNSUPPORTED;
+    }
+    return TT_OK;
+}
+
+// No output overlaps another output, or an input other than its own.
+tt_status check_clip_overlap(const ClipList& l) {
+    struct Range {
+        uintptr_t lo, hi;
+        bool out;
+        bool operator<(const Range& o) const { return lo < o.lo; }
+    };
+    Range* r = static_cast<Range*>(malloc(sizeof(Range) * 2 * (size_t)(l.count > 0 ? l.count : 1)));
+    if (r == nullptr) return TT_ERR_NO_MEMORY;
+    int k = 0;
+    for (int i = 0; i < l.count; ++i) {
+        if (l.n[i] == 0) continue;
+        const size_t bytes = (size_t)l.n[i] * elem_bytes(l.dtype[i]);
+        const uintptr_t in = reinterpret_cast<uintptr_t>(l.in[i]), out = reinterpret_cast<uintptr_t>(l.out[i]);
+        r[k++] = {out, out + bytes, true};
+        if (in != out) r[k++] = {in, in + bytes, false};
+    }
+    if (!std::is_sorted(r, r + k)) std::sort(r, r + k);
+    uintptr_t out_end = 0, in_end = 0;
+    bool bad = false;
+    for (int i = 0; i < k && !bad; ++i) {
+        bad = r[i].lo < out_end || (r[i].out && r[i].lo < in_end);
+        uintptr_t& end = r[i].out ? out_end : in_end;
+        if (r[i].hi > end) end = r[i].hi;
+    }
+    free(r);
+    if (bad) set_last_error_message("an output overlaps another tensor of the call");
+    return bad ? TT_ERR_INVALID_ARG : TT_OK;
+}
+
+tt_status clip(const ClipList& l, bool scale, float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+               void* stream) {
+    tt_status st = check_clip_list(l.count, l.n, l.dtype);
+    if (st != TT_OK) return st;
+    if (l.count > 0 && (l.in == nullptr || l.out == nullptr)) return TT_ERR_INVALID_ARG;
+    if (!(max_norm >= 0.0f) || norm == nullptr || !aligned(norm, 4)) return TT_ERR_INVALID_ARG;
+    for (int i = 0; i < l.count; ++i) {
+        if (l.n[i] == 0) continue;
+        if (l.in[i] == nullptr || !aligned(l.in[i], elem_bytes(l.dtype[i]))) return TT_ERR_INVALID_ARG;
+        if (scale && (l.out[i] == nullptr || !aligned(l.out[i], elem_bytes(l.dtype[i])))) return TT_ERR_INVALID_ARG;
+    }
+    const int sms = sm_count_current();
+    const size_t need = clip_workspace_bytes(l, sms);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != TT_OK) return st;
+    if (scale && (st = check_clip_overlap(l)) != TT_OK) return st;
+    for (int i = 0; i < l.count; ++i) {
+        if (l.n[i] == 0) continue;
+        const size_t bytes = (size_t)l.n[i] * elem_bytes(l.dtype[i]);
+        if (overlap(l.in[i], bytes, norm, 4) || overlap(l.in[i], bytes, workspace, need) ||
+            (scale && (overlap(l.out[i], bytes, norm, 4) || overlap(l.out[i], bytes, workspace, need)))) {
+            set_last_error_message("norm or workspace overlaps a tensor");
+            return TT_ERR_INVALID_ARG;
+        }
+        if ((st = check_device_ptr(l.in[i], "grads")) != TT_OK) return st;
+        if (scale && l.out[i] != l.in[i] && (st = check_device_ptr(l.out[i], "out")) != TT_OK) return st;
+    }
+    if (overlap(norm, 4, workspace, need)) return TT_ERR_INVALID_ARG;
+    if ((st = check_device_ptr(norm, "norm")) != TT_OK) return st;
+    if ((st = check_device_ptr(workspace, "workspace")) != TT_OK) return st;
+    const cudaError_t e = launch_clip(l, scale, max_norm, norm, static_cast<double*>(workspace),
+                                      static_cast<cudaStream_t>(stream), sms);
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "gradient norm");
 }
 
 }  // namespace
@@ -160,6 +236,27 @@ tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x,
     const cudaError_t e = launch_normalize_grad(grad_y, g_dtype, x, dtype, n, d, grad_x,
                                                 static_cast<cudaStream_t>(stream), sm_count_current());
     return e == cudaSuccess ? TT_OK : cuda_fail(e, "normalisation gradient");
+}
+
+tt_status tt_clip_grad_norm_workspace(int32_t count, const int64_t* n, const int32_t* dtypes, size_t* bytes) {
+    if (bytes == nullptr) return TT_ERR_INVALID_ARG;
+    const tt_status st = check_clip_list(count, n, dtypes);
+    if (st != TT_OK) return st;
+    *bytes = clip_workspace_bytes({count, nullptr, nullptr, n, dtypes}, sm_count_current());
+    return TT_OK;
+}
+
+tt_status tt_grad_norm(int32_t count, const void* const* grads, const int64_t* n, const int32_t* dtypes, float* norm,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    return clip({count, grads, const_cast<void* const*>(grads), n, dtypes}, false, 0.0f, norm, workspace,
+                workspace_bytes, stream);
+}
+
+tt_status tt_clip_grad_norm(int32_t count, const void* const* grads, const int64_t* n, const int32_t* dtypes,
+                            void* const* out, float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+    return clip({count, grads, out != nullptr ? out : const_cast<void* const*>(grads), n, dtypes}, true, max_norm, norm,
+                workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -485,6 +485,40 @@ TT_API tt_status tt_layernorm_grad(const void* grad_y, const void* x, tt_dtype d
 TT_API tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x, tt_dtype dtype, int64_t n,
                                    int32_t d, void* grad_x, void* stream);
 
+/*
+ * tt_grad_norm, tt_clip_grad_norm - the global L2 norm of many tensors, and
+ * their scaling to at most a given norm.
+ *
+ *   norm  = sqrt(sum of x^2 over all elements of all tensors)
+ *   scale = min(1, max_norm / (norm + 1e-6))
+ *   out   = x scale, rounded to the tensor's dtype  (tt_clip_grad_norm)
+ *
+ * The squares are summed in fp64 (groups of eight in fp32 where they neither
+ * overflow nor underflow there); norm and scale are fp32. A norm that is NaN
+ * makes every element NaN, an infinite one makes scale 0 (and an infinite
+ * element NaN), as the formula says.
+ *
+ * count      tensors, >= 0 (0: the norm is 0)
+ * grads      HOST array of device pointers, aligned to their element size
+ *            (a tensor may begin anywhere in a flat buffer; 16-byte alignment
+ *            of grads and out is fastest)
+ * n          HOST array of element counts, each 0 <= n < 2^42
+ * dtypes     HOST array of tt_dtype, each TT_F32 or TT_BF16
+ * out        HOST array of device pointers, or NULL to scale in place.
+ *            out[i] may be grads[i]; apart from that no output may overlap
+ *            anything (so no tensor may be listed twice in place).
+ * max_norm   >= 0 (may be infinite: nothing is scaled)
+ * norm       device f32 [1]: the norm before the scaling
+ * workspace  tt_clip_grad_norm_workspace bytes (for both calls)
+ * The host arrays are read before the call returns.
+ */
+TT_API tt_status tt_clip_grad_norm_workspace(int32_t count, const int64_t* n, const int32_t* dtypes, size_t* bytes);
+TT_API tt_status tt_grad_norm(int32_t count, const void* const* grads, const int64_t* n, const int32_t* dtypes,
+                              float* norm, void* workspace, size_t workspace_bytes, void* stream);
+TT_API tt_status tt_clip_grad_norm(int32_t count, const void* const* grads, const int64_t* n, const int32_t* dtypes,
+                                   void* const* out, float max_norm, float* norm, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
 /* Release a handle. Its work memory returns to a per-device pool that later
  * handles reuse (it is not returned to CUDA before the process exits); a
  * later user's stream first waits for the work this handle had enqueued, so
@@ -545,7 +579,8 @@ TT_API tt_status tt_score_topk_noalloc(const void* rows, tt_dtype dtype, int64_t
 #define TT_KIND_SOFTMAX 6  /* tt_inbatch_softmax */
 #define TT_KIND_ESTIMATE 7 /* the sampled threshold estimate of a small batch */
 #define TT_KIND_ROWNORM 8  /* layer norm, and the gradients of the row norms */
-#define TT_NUM_KINDS 9
+#define TT_KIND_CLIP 9     /* the global norm and clipping */
+#define TT_NUM_KINDS 10
 
 /* Total kernels this library has launched in the process. */
 TT_API int64_t tt_launch_count(void);

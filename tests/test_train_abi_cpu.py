@@ -56,3 +56,38 @@ def test_normalize_grad_arguments():
     assert call(dy=None) == INV and call(x=None) == INV and call(gx=None) == INV and call(gx=ODD) == INV
     assert call(gx=P[0]) == INV and call(gx=P[1]) == INV
     assert call(n=0, dy=None, x=None, gx=None) == tt.TT_OK
+
+
+def _list(kind, values):
+    return (kind * max(1, len(values)))(*values)
+
+
+def test_clip_arguments():
+    A, B = 0x1000000, 0x2000000
+    size = ctypes.c_size_t(0)
+    n2, f2 = _list(ctypes.c_int64, [100, 200]), _list(ctypes.c_int32, [0, 1])
+    assert tt._lib.tt_clip_grad_norm_workspace(2, n2, f2, None) == INV
+    assert tt._lib.tt_clip_grad_norm_workspace(-1, n2, f2, ctypes.byref(size)) == INV
+    assert tt._lib.tt_clip_grad_norm_workspace(2, None, f2, ctypes.byref(size)) == INV
+    assert tt._lib.tt_clip_grad_norm_workspace(2, n2, f2, ctypes.byref(size)) == tt.TT_OK
+    need = size.value
+
+    def call(count=2, ins=(A, B), n=(100, 200), dt=(0, 1), outs=None, max_norm=1.0, norm=P[5], ws=P[6], size=need):
+        outs = None if outs is None else _list(ctypes.c_void_p, outs)
+        return tt._lib.tt_clip_grad_norm(count, _list(ctypes.c_void_p, ins), _list(ctypes.c_int64, n),
+                                         _list(ctypes.c_int32, dt), outs, max_norm, norm, ws, size, None)
+
+    assert call(count=-1) == INV and call(n=(100, -1)) == INV and call(n=(100, 1 << 42)) == UNS
+    assert call(dt=(0, tt.TT_I8)) == INV and call(dt=(0, 9)) == INV
+    assert call(max_norm=-1.0) == INV and call(max_norm=float("nan")) == INV
+    assert call(norm=None) == INV and call(ws=None) == INV and call(ws=ODD) == INV and call(size=need - 1) == INV
+    assert call(ins=(A, None)) == INV and call(ins=(A + 2, B)) == INV and call(ins=(A, B + 1)) == INV
+    assert call(ins=(A, A)) == INV                      # one tensor twice, in place
+    assert call(ins=(A, A + 396)) == INV                # the last element of the first
+    assert call(outs=(A, A)) == INV and call(outs=(B, A)) == INV  # an output over another tensor's input
+    assert call(outs=(A + 4, 0x3000000)) == INV         # an output over its own input, shifted
+    assert call(norm=ctypes.c_void_p(A + 8)) == INV and call(ws=ctypes.c_void_p(A & ~255)) == INV
+    # the norm alone takes the same tensor twice; its other arguments are checked alike
+    grad_norm = lambda ins=(A, B), norm=P[5], ws=P[6], size=need: tt._lib.tt_grad_norm(  # noqa: E731
+        2, _list(ctypes.c_void_p, ins), n2, f2, norm, ws, size, None)
+    assert grad_norm(ins=(None, B)) == INV and grad_norm(norm=None) == INV and grad_norm(size=need - 1) == INV
