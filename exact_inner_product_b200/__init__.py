@@ -40,7 +40,7 @@ TT_MAX_K = 2048
 TT_MAX_WIDTH = 16384
 
 KIND_NAMES = ("normalize", "cast", "stream", "tensor", "select", "aux", "softmax", "estimate",
-              "rownorm", "clip")
+              "rownorm", "clip", "embedding")
 TT_NUM_KINDS = len(KIND_NAMES)
 
 if not os.path.exists(LIB_PATH):
@@ -107,6 +107,13 @@ _sig("tt_normalize_grad", ctypes.c_int, [_vp, ctypes.c_int, _vp, ctypes.c_int, _
 _sig("tt_clip_grad_norm_workspace", ctypes.c_int, [_i32, _vp, _vp, ctypes.POINTER(ctypes.c_size_t)])
 _sig("tt_grad_norm", ctypes.c_int, [_i32, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp])
 _sig("tt_clip_grad_norm", ctypes.c_int, [_i32, _vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, ctypes.c_size_t, _vp])
+_sig("tt_embedding", ctypes.c_int, [_vp, ctypes.c_int, _i64, _i32, _vp, _i32, _i64, ctypes.c_float, _vp, ctypes.c_int,
+                                    _vp])
+_sig("tt_embedding_grad_workspace", ctypes.c_int, [_i64, _i64, _i32, ctypes.POINTER(ctypes.c_size_t)])
+_sig("tt_embedding_grad", ctypes.c_int, [_vp, _i32, _i64, _vp, ctypes.c_int, _i64, _i32, ctypes.c_float, _vp,
+                                         ctypes.c_int, _vp, ctypes.c_size_t, _vp])
+_sig("tt_embedding_grad_rows", ctypes.c_int, [_vp, _i32, _i64, _vp, ctypes.c_int, _i64, _i32, ctypes.c_float, _vp, _vp,
+                                              ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp])
 _sig("tt_free", None, [_vp])
 _sig("tt_launch_count", _i64, [])
 _sig("tt_profile_begin", ctypes.c_int, [])
@@ -122,6 +129,7 @@ EXPORTED = ("tt_normalize_candidates", "tt_quantize_candidates", "tt_index_wrap"
             "tt_score_topk_noalloc", "tt_merge_topk", "tt_score_topk_ranges", "tt_score_topk_types",
             "tt_inbatch_softmax_workspace", "tt_inbatch_softmax", "tt_inbatch_softmax_check",
             "tt_layernorm", "tt_layernorm_grad_workspace", "tt_layernorm_grad", "tt_normalize_grad",
+            "tt_embedding", "tt_embedding_grad_workspace", "tt_embedding_grad", "tt_embedding_grad_rows",
             "tt_clip_grad_norm_workspace", "tt_grad_norm", "tt_clip_grad_norm",
             "tt_last_stats", "tt_plan", "tt_free", "tt_launch_count", "tt_profile_begin",
             "tt_profile_end", "tt_profile_launches", "tt_status_string", "tt_last_error", "tt_version")
@@ -531,6 +539,87 @@ def tt_normalize_grad(grad_y: torch.Tensor, x: torch.Tensor, out: torch.Tensor |
     _check(_lib.tt_normalize_grad(_ptr(grad_y), _dtype(grad_y), _ptr(x), _dtype(x), n, d, _ptr(out), _stream(stream)),
            "tt_normalize_grad")
     return out
+
+
+_IDS = (torch.int32, torch.int64)
+
+
+def tt_embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out: torch.Tensor | None = None,
+                 out_dtype=None, stream=None) -> torch.Tensor:
+    """Rows of ``table`` [rows, d] by ``ids`` (int32 or int64, any shape), times
+    ``scale`` (``tt_embedding``). An id outside [0, rows), such as the padding
+    id -1 of a search, gives a row of zeros. Returns [*ids.shape, d] in
+    ``out_dtype`` (default: the table's)."""
+    if table.dim() != 2:
+        raise ValueError("table must be [rows, d]")
+    _check_float("table", table)
+    _check_float("ids", ids, dtypes=_IDS, device=table.device)
+    rows, d = table.shape
+    if out is None:
+        out = torch.empty((*ids.shape, d), dtype=out_dtype or table.dtype, device=table.device)
+    _check_float("out", out, (*ids.shape, d), (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,),
+                 table.device)
+    _check(_lib.tt_embedding(_ptr(table), _dtype(table), rows, d, _ptr(ids), ids.element_size(), ids.numel(),
+                             float(scale), _ptr(out), _dtype(out), _stream(stream)), "tt_embedding")
+    return out
+
+
+def tt_embedding_grad_workspace(m: int, rows: int, d: int) -> int:
+    """Bytes of device workspace ``tt_embedding_grad`` and ``tt_embedding_grad_rows`` need."""
+    need = ctypes.c_size_t(0)
+    _check(_lib.tt_embedding_grad_workspace(int(m), int(rows), int(d), ctypes.byref(need)),
+           "tt_embedding_grad_workspace")
+    return int(need.value)
+
+
+def _embedding_grad_args(ids, grad, rows, workspace):
+    if grad.dim() < 1 or grad.shape[:-1] != ids.shape:
+        raise ValueError(f"grad must be [*ids.shape, d], got {tuple(grad.shape)} for ids {tuple(ids.shape)}")
+    _check_float("grad", grad)
+    _check_float("ids", ids, dtypes=_IDS, device=grad.device)
+    m, d = ids.numel(), grad.shape[-1]
+    return m, d, _workspace(workspace, tt_embedding_grad_workspace(m, rows, d) if workspace is None else 0, grad.device)
+
+
+def tt_embedding_grad(ids: torch.Tensor, grad: torch.Tensor, rows: int, scale: float = 1.0,
+                      out: torch.Tensor | None = None, out_dtype=None, workspace: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """The gradient of ``tt_embedding`` with respect to the table
+    (``tt_embedding_grad``): ``grad`` is [*ids.shape, d]. Returns [rows, d] in
+    ``out_dtype`` (default: grad's), zeros where no id points."""
+    m, d, workspace = _embedding_grad_args(ids, grad, rows, workspace)
+    if out is None:
+        out = torch.empty((rows, d), dtype=out_dtype or grad.dtype, device=grad.device)
+    _check_float("out", out, (rows, d), (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,),
+                 grad.device)
+    _check(_lib.tt_embedding_grad(_ptr(ids), ids.element_size(), m, _ptr(grad), _dtype(grad), int(rows), d, float(scale),
+                                  _ptr(out), _dtype(out), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "tt_embedding_grad")
+    return out
+
+
+def tt_embedding_grad_rows(ids: torch.Tensor, grad: torch.Tensor, rows: int, scale: float = 1.0,
+                           out: tuple | None = None, out_dtype=None, count: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """The same gradient as the rows of the ids that occur
+    (``tt_embedding_grad_rows``): returns ``(ids [m], rows [m, d], count [1])``
+    with m = ids.numel(). The first ``count`` entries hold the ids, ascending,
+    and their rows; what lies behind them is left as it was. ``out`` gives the
+    first two tensors."""
+    m, d, workspace = _embedding_grad_args(ids, grad, rows, workspace)
+    dev = grad.device
+    if out is None:
+        out = (torch.empty(m, dtype=ids.dtype, device=dev),
+               torch.empty((m, d), dtype=out_dtype or grad.dtype, device=dev))
+    _check_float("out ids", out[0], (m,), (ids.dtype,), dev)
+    _check_float("out rows", out[1], (m, d), (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,), dev)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=dev)
+    _check_float("count", count, (1,), (torch.int32,), dev)
+    _check(_lib.tt_embedding_grad_rows(_ptr(ids), ids.element_size(), m, _ptr(grad), _dtype(grad), int(rows), d,
+                                       float(scale), _ptr(out[0]), _ptr(out[1]), _dtype(out[1]), _ptr(count),
+                                       _ptr(workspace), workspace.numel(), _stream(stream)), "tt_embedding_grad_rows")
+    return out[0], out[1], count
 
 
 _ELEM = {torch.float32: TT_F32, torch.bfloat16: TT_BF16}

@@ -285,4 +285,24 @@ size_t clip_workspace_bytes(const ClipList& l, int sm_count);
 cudaError_t launch_clip(const ClipList& l, bool scale, float max_norm, float* norm, double* part, cudaStream_t s,
                         int sm_count);
 
+// Embedding lookup and its gradient (k_embedding.cu). id_bytes: 4 or 8.
+cudaError_t launch_embedding(const void* table, int table_dtype, int64_t rows, int d, const void* ids, int id_bytes,
+                             int64_t m, float scale, void* out, int out_dtype, cudaStream_t s, int sm_count);
+struct EmbeddingGrad {
+    const void* ids;   // [m]
+    int id_bytes;
+    int64_t m, rows;
+    const void* grad;  // [m, d]
+    int grad_dtype;
+    int d;
+    float scale;
+    void* out;         // [rows, d]: a row for every id; by_row: [m, d]
+    int out_dtype;
+    void* out_ids;     // by_row: [m] of the ids' type
+    int32_t* count;    // by_row: rows written
+    void* workspace;   // embedding_grad_bytes
+};
+size_t embedding_grad_bytes(int64_t m, int64_t rows, int d);
+cudaError_t launch_embedding_grad(const EmbeddingGrad& g, bool by_row, cudaStream_t s, int sm_count);
+
 }  // namespace tt

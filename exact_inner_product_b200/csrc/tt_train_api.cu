@@ -147,6 +147,39 @@ tt_status clip(const ClipList& l, bool scale, float max_norm, float* norm, void*
     return e == cudaSuccess ? TT_OK : cuda_fail(e, "gradient norm");
 }
 
+tt_status check_embedding(int64_t rows, int32_t d, int32_t id_bytes, int64_t m, float scale) {
+    tt_status st = check_rows(rows, d);
+    if (st != TT_OK) return st;
+    if ((st = check_rows(m, d)) != TT_OK) return st;
+    if ((id_bytes != 4 && id_bytes != 8) || !isfinite(scale)) return TT_ERR_INVALID_ARG;
+    return TT_OK;
+}
+
+tt_status embedding_grad(const EmbeddingGrad& g, bool by_row, size_t workspace_bytes, void* stream) {
+    tt_status st = check_embedding(g.rows, g.d, g.id_bytes, g.m, g.scale);
+    if (st != TT_OK) return st;
+    if (!valid_dtype(g.grad_dtype) || !valid_dtype(g.out_dtype)) return TT_ERR_INVALID_ARG;
+    if (!aligned(g.ids, g.id_bytes) || !aligned(g.grad, 16) || !aligned(g.out, 16) || !aligned(g.out_ids, g.id_bytes) ||
+        !aligned(g.count, 4))
+        return TT_ERR_INVALID_ARG;
+    if (g.m > 0 && (g.ids == nullptr || g.grad == nullptr)) return TT_ERR_INVALID_ARG;
+    if (by_row ? (g.count == nullptr || (g.m > 0 && (g.out == nullptr || g.out_ids == nullptr)))
+               : (g.rows > 0 && g.out == nullptr))
+        return TT_ERR_INVALID_ARG;
+    const size_t need = embedding_grad_bytes(g.m, g.rows, g.d);
+    if ((st = check_workspace(g.workspace, workspace_bytes, need)) != TT_OK) return st;
+    Buffers b;
+    b.in(g.ids, (size_t)g.m * g.id_bytes, "ids");
+    b.in(g.grad, (size_t)g.m * g.d * elem_bytes(g.grad_dtype), "grad");
+    b.out(g.out, (size_t)(by_row ? g.m : g.rows) * g.d * elem_bytes(g.out_dtype), by_row ? "out_rows" : "grad_table");
+    b.out(g.out_ids, (size_t)g.m * g.id_bytes, "out_ids");
+    b.out(g.count, sizeof(int32_t), "count");
+    b.out(g.workspace, need, "workspace");
+    if ((st = b.check()) != TT_OK) return st;
+    const cudaError_t e = launch_embedding_grad(g, by_row, static_cast<cudaStream_t>(stream), sm_count_current());
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "embedding gradient");
+}
+
 }  // namespace
 }  // namespace tt
 
@@ -257,6 +290,49 @@ tt_status tt_clip_grad_norm(int32_t count, const void* const* grads, const int64
                             void* stream) {
     return clip({count, grads, out != nullptr ? out : const_cast<void* const*>(grads), n, dtypes}, true, max_norm, norm,
                 workspace, workspace_bytes, stream);
+}
+
+tt_status tt_embedding(const void* table, tt_dtype table_dtype, int64_t rows, int32_t d, const void* ids,
+                       int32_t id_bytes, int64_t m, float scale, void* out, tt_dtype out_dtype, void* stream) {
+    tt_status st = check_embedding(rows, d, id_bytes, m, scale);
+    if (st != TT_OK) return st;
+    if (!valid_dtype(table_dtype) || !valid_dtype(out_dtype)) return TT_ERR_INVALID_ARG;
+    if (!aligned(table, 16) || !aligned(ids, id_bytes) || !aligned(out, 16)) return TT_ERR_INVALID_ARG;
+    if (m == 0) return TT_OK;
+    if ((rows > 0 && table == nullptr) || ids == nullptr || out == nullptr) return TT_ERR_INVALID_ARG;
+    Buffers b;
+    b.in(table, (size_t)rows * d * elem_bytes(table_dtype), "table");
+    b.in(ids, (size_t)m * id_bytes, "ids");
+    b.out(out, (size_t)m * d * elem_bytes(out_dtype), "out");
+    if ((st = b.check()) != TT_OK) return st;
+    const cudaError_t e = launch_embedding(table, table_dtype, rows, d, ids, id_bytes, m, scale, out, out_dtype,
+                                           static_cast<cudaStream_t>(stream), sm_count_current());
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "embedding lookup");
+}
+
+tt_status tt_embedding_grad_workspace(int64_t m, int64_t rows, int32_t d, size_t* bytes) {
+    if (bytes == nullptr) return TT_ERR_INVALID_ARG;
+    const tt_status st = check_embedding(rows, d, 4, m, 1.0f);
+    if (st != TT_OK) return st;
+    *bytes = embedding_grad_bytes(m, rows, d);
+    return TT_OK;
+}
+
+tt_status tt_embedding_grad(const void* ids, int32_t id_bytes, int64_t m, const void* grad, tt_dtype grad_dtype,
+                            int64_t rows, int32_t d, float scale, void* grad_table, tt_dtype out_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    return embedding_grad({ids, id_bytes, m, rows, grad, grad_dtype, d, scale, grad_table, out_dtype, nullptr, nullptr,
+                           workspace},
+                          false, workspace_bytes, stream);
+}
+
+tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64_t m, const void* grad, tt_dtype grad_dtype,
+                                 int64_t rows, int32_t d, float scale, void* out_ids, void* out_rows,
+                                 tt_dtype out_dtype, int32_t* count, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+    return embedding_grad({ids, id_bytes, m, rows, grad, grad_dtype, d, scale, out_rows, out_dtype, out_ids, count,
+                           workspace},
+                          true, workspace_bytes, stream);
 }
 
 }  // extern "C"

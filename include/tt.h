@@ -519,6 +519,54 @@ TT_API tt_status tt_clip_grad_norm(int32_t count, const void* const* grads, cons
                                    void* const* out, float max_norm, float* norm, void* workspace,
                                    size_t workspace_bytes, void* stream);
 
+/*
+ * tt_embedding - rows of a table by id, scaled.
+ *
+ *   out_t = scale * table[ids_t], rounded to out_dtype; zeros where ids_t is
+ *   not in [0, rows) (tt_score_topk's padding id -1 among them, so its out_ids
+ *   can be looked up as they are)
+ *
+ * table      device [rows, d] table_dtype (TT_F32 or TT_BF16)
+ * rows       0 <= rows < 2^31
+ * d          1 <= d <= TT_MAX_WIDTH, any value (multiples of 8 are fastest)
+ * ids        device [m] int32 (id_bytes 4) or int64 (id_bytes 8)
+ * m          0 <= m < 2^31
+ * scale      finite
+ * out        device [m, d] out_dtype (TT_F32 or TT_BF16)
+ */
+TT_API tt_status tt_embedding(const void* table, tt_dtype table_dtype, int64_t rows, int32_t d, const void* ids,
+                              int32_t id_bytes, int64_t m, float scale, void* out, tt_dtype out_dtype, void* stream);
+
+/*
+ * tt_embedding_grad - the gradient of tt_embedding with respect to the table:
+ *
+ *   grad_table_r = scale * sum over t with ids_t = r of grad_t
+ *
+ * summed in fp32 in an order that the ids fix (no atomic additions), rounded
+ * once to out_dtype. Ids outside [0, rows) add nothing, and their rows of
+ * grad are not read.
+ *
+ * grad        device [m, d] grad_dtype (TT_F32 or TT_BF16)
+ * grad_table  device [rows, d] out_dtype: every row is written (zeros where
+ *             no id points)
+ * workspace   tt_embedding_grad_workspace bytes (for both forms)
+ * other arguments as tt_embedding
+ *
+ * tt_embedding_grad_rows - the same as rows of the ids that occur:
+ * out_ids      device [m], of the ids' type: the ids that occur, ascending
+ * out_rows     device [m, d] out_dtype: row q belongs to out_ids[q]
+ * count        device int32 [1]: how many there are. Entries of out_ids and
+ *              out_rows from there on are left as they were.
+ */
+TT_API tt_status tt_embedding_grad_workspace(int64_t m, int64_t rows, int32_t d, size_t* bytes);
+TT_API tt_status tt_embedding_grad(const void* ids, int32_t id_bytes, int64_t m, const void* grad, tt_dtype grad_dtype,
+                                   int64_t rows, int32_t d, float scale, void* grad_table, tt_dtype out_dtype,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+TT_API tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64_t m, const void* grad,
+                                        tt_dtype grad_dtype, int64_t rows, int32_t d, float scale, void* out_ids,
+                                        void* out_rows, tt_dtype out_dtype, int32_t* count, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
 /* Release a handle. Its work memory returns to a per-device pool that later
  * handles reuse (it is not returned to CUDA before the process exits); a
  * later user's stream first waits for the work this handle had enqueued, so
@@ -580,7 +628,8 @@ TT_API tt_status tt_score_topk_noalloc(const void* rows, tt_dtype dtype, int64_t
 #define TT_KIND_ESTIMATE 7 /* the sampled threshold estimate of a small batch */
 #define TT_KIND_ROWNORM 8  /* layer norm, and the gradients of the row norms */
 #define TT_KIND_CLIP 9     /* the global norm and clipping */
-#define TT_NUM_KINDS 10
+#define TT_KIND_EMBEDDING 10 /* embedding lookup and its gradient */
+#define TT_NUM_KINDS 11
 
 /* Total kernels this library has launched in the process. */
 TT_API int64_t tt_launch_count(void);

@@ -91,3 +91,43 @@ def test_clip_arguments():
     grad_norm = lambda ins=(A, B), norm=P[5], ws=P[6], size=need: tt._lib.tt_grad_norm(  # noqa: E731
         2, _list(ctypes.c_void_p, ins), n2, f2, norm, ws, size, None)
     assert grad_norm(ins=(None, B)) == INV and grad_norm(norm=None) == INV and grad_norm(size=need - 1) == INV
+
+
+def test_embedding_arguments():
+    def call(table=P[0], dt=0, rows=10, d=64, ids=P[1], id_bytes=8, m=4, scale=1.0, out=P[2], odt=0):
+        return tt._lib.tt_embedding(table, dt, rows, d, ids, id_bytes, m, scale, out, odt, None)
+
+    assert call(rows=-1) == INV and call(d=0) == INV and call(m=-1) == INV
+    assert call(rows=1 << 31) == UNS and call(d=tt.TT_MAX_WIDTH + 1) == UNS and call(m=1 << 31) == UNS
+    assert call(id_bytes=2) == INV and call(scale=float("nan")) == INV and call(scale=float("inf")) == INV
+    assert call(dt=tt.TT_I8) == INV and call(odt=8) == INV
+    assert call(table=None) == INV and call(ids=None) == INV and call(out=None) == INV
+    assert call(table=ODD) == INV and call(out=ODD) == INV and call(ids=ctypes.c_void_p(0x1000004)) == INV
+    assert call(out=P[0]) == INV and call(out=ctypes.c_void_p(P[1].value + 16)) == INV
+    assert call(m=0, table=None, ids=None, out=None) == tt.TT_OK
+
+
+def test_embedding_grad_arguments():
+    size = ctypes.c_size_t(0)
+    assert tt._lib.tt_embedding_grad_workspace(4, 10, 64, None) == INV
+    assert tt._lib.tt_embedding_grad_workspace(-4, 10, 64, ctypes.byref(size)) == INV
+    assert tt._lib.tt_embedding_grad_workspace(4, 10, 64, ctypes.byref(size)) == tt.TT_OK
+    need = size.value
+
+    def dense(ids=P[0], id_bytes=4, m=4, grad=P[1], dt=0, rows=10, d=64, scale=1.0, out=P[2], odt=0, ws=P[3], size=need):
+        return tt._lib.tt_embedding_grad(ids, id_bytes, m, grad, dt, rows, d, scale, out, odt, ws, size, None)
+
+    def by_row(ids=P[0], id_bytes=4, m=4, grad=P[1], dt=0, rows=10, d=64, scale=1.0, oids=P[2], out=P[3], odt=0,
+               count=P[4], ws=P[5], size=need):
+        return tt._lib.tt_embedding_grad_rows(ids, id_bytes, m, grad, dt, rows, d, scale, oids, out, odt, count, ws, size,
+                                              None)
+
+    for call in (dense, by_row):
+        assert call(rows=-1) == INV and call(rows=1 << 31) == UNS and call(m=-1) == INV and call(m=1 << 31) == UNS
+        assert call(d=0) == INV and call(d=20000) == UNS and call(id_bytes=1) == INV and call(scale=float("nan")) == INV
+        assert call(dt=tt.TT_I8) == INV and call(odt=tt.TT_I8) == INV
+        assert call(ids=None) == INV and call(grad=None) == INV and call(out=None) == INV
+        assert call(ids=ODD) == INV and call(grad=ODD) == INV and call(out=ODD) == INV
+        assert call(ws=None) == INV and call(ws=ODD) == INV and call(size=need - 1) == INV
+        assert call(out=P[1]) == INV and call(ws=P[1]) == INV
+    assert by_row(oids=None) == INV and by_row(count=None) == INV and by_row(oids=P[0]) == INV and by_row(count=P[2]) == INV
