@@ -40,7 +40,7 @@ TT_MAX_K = 2048
 TT_MAX_WIDTH = 16384
 
 KIND_NAMES = ("normalize", "cast", "stream", "tensor", "select", "aux", "softmax", "estimate",
-              "rownorm", "clip", "embedding")
+              "rownorm", "clip", "embedding", "softmax_grad")
 TT_NUM_KINDS = len(KIND_NAMES)
 
 if not os.path.exists(LIB_PATH):
@@ -114,6 +114,9 @@ _sig("tt_embedding_grad", ctypes.c_int, [_vp, _i32, _i64, _vp, ctypes.c_int, _i6
                                          ctypes.c_int, _vp, ctypes.c_size_t, _vp])
 _sig("tt_embedding_grad_rows", ctypes.c_int, [_vp, _i32, _i64, _vp, ctypes.c_int, _i64, _i32, ctypes.c_float, _vp, _vp,
                                               ctypes.c_int, _vp, _vp, ctypes.c_size_t, _vp])
+_sig("tt_inbatch_softmax_grad_workspace", ctypes.c_int, [_i32, _i32, _i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)])
+_sig("tt_inbatch_softmax_grad", ctypes.c_int, [_vp, _vp, ctypes.c_int, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                               _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp])
 _sig("tt_free", None, [_vp])
 _sig("tt_launch_count", _i64, [])
 _sig("tt_profile_begin", ctypes.c_int, [])
@@ -130,6 +133,7 @@ EXPORTED = ("tt_normalize_candidates", "tt_quantize_candidates", "tt_index_wrap"
             "tt_inbatch_softmax_workspace", "tt_inbatch_softmax", "tt_inbatch_softmax_check",
             "tt_layernorm", "tt_layernorm_grad_workspace", "tt_layernorm_grad", "tt_normalize_grad",
             "tt_embedding", "tt_embedding_grad_workspace", "tt_embedding_grad", "tt_embedding_grad_rows",
+            "tt_inbatch_softmax_grad_workspace", "tt_inbatch_softmax_grad",
             "tt_clip_grad_norm_workspace", "tt_grad_norm", "tt_clip_grad_norm",
             "tt_last_stats", "tt_plan", "tt_free", "tt_launch_count", "tt_profile_begin",
             "tt_profile_end", "tt_profile_launches", "tt_status_string", "tt_last_error", "tt_version")
@@ -692,6 +696,68 @@ def tt_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | Non
     _check(_lib.tt_clip_grad_norm(count, ptrs, n, dtypes, outs, float(max_norm), _ptr(norm), _ptr(workspace),
                                   workspace.numel(), _stream(stream)), "tt_clip_grad_norm")
     return norm
+
+
+def tt_inbatch_softmax_grad_workspace(b: int, nc: int, d: int, with_item_ids: bool, with_valid: bool) -> int:
+    """Bytes of device workspace ``tt_inbatch_softmax_grad`` needs for these sizes."""
+    need = ctypes.c_size_t(0)
+    _check(_lib.tt_inbatch_softmax_grad_workspace(int(b), int(nc), int(d), 1 if with_item_ids else 0,
+                                                  1 if with_valid else 0, ctypes.byref(need)),
+           "tt_inbatch_softmax_grad_workspace")
+    return int(need.value)
+
+
+def tt_inbatch_softmax_grad(users: torch.Tensor, items: torch.Tensor, lse: torch.Tensor, loss: torch.Tensor,
+                            tau: float = 1.0, logq: torch.Tensor | None = None, item_ids: torch.Tensor | None = None,
+                            valid: torch.Tensor | None = None, grad_loss: torch.Tensor | None = None,
+                            grad_mean: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                            out: tuple | None = None, stream=None, check: bool = False):
+    """The gradient of ``tt_inbatch_softmax`` with respect to users and items
+    (``tt_inbatch_softmax_grad``). ``users`` to ``valid`` are the loss call's
+    arguments, ``lse`` and ``loss`` [b] its results; ``grad_loss`` float32 [b]
+    and ``grad_mean`` (one float32) the gradients of its loss rows and of its
+    mean (at least one of them). Returns ``(grad_users [b, d], grad_items [nc,
+    d])`` in bfloat16. ``workspace`` (uint8) and ``out`` may be passed to avoid
+    allocations; ``check`` waits for the result and raises on a device-side
+    timeout (without it, every output is NaN after one)."""
+    if users.dim() != 2 or items.dim() != 2:
+        raise ValueError("users and items must be [b, d] and [nc, d] tensors")
+    b, d = users.shape
+    nc = items.shape[0]
+    dev = users.device
+    _check_float("users", users)
+    _check_float("items", items, (nc, d), (users.dtype,), dev)
+    for name, t, shape, dt in (("lse", lse, (b,), torch.float32), ("loss", loss, (b,), torch.float32),
+                               ("logq", logq, (nc,), torch.float32), ("item_ids", item_ids, (nc,), torch.int64),
+                               ("grad_loss", grad_loss, (b,), torch.float32)):
+        if t is not None:
+            _check_float(name, t, shape, (dt,), dev)
+    if valid is not None:
+        if valid.dtype == torch.bool:
+            valid = valid.view(torch.uint8)
+        _check_float("valid", valid, (nc,), (torch.uint8,), dev)
+    if grad_loss is None and grad_mean is None:
+        raise ValueError("grad_loss or grad_mean must be given")
+    if grad_mean is not None:
+        _check_float("grad_mean", grad_mean, dtypes=(torch.float32,), device=dev)
+        if grad_mean.numel() != 1:
+            raise ValueError("grad_mean must hold one number")
+    need = 0
+    if workspace is None:
+        need = tt_inbatch_softmax_grad_workspace(b, nc, d, item_ids is not None, valid is not None)
+    workspace = _workspace(workspace, need, dev)
+    if out is None:
+        out = (torch.empty_like(users), torch.empty_like(items))
+    else:
+        _check_float("out grad_users", out[0], (b, d), (users.dtype,), dev)
+        _check_float("out grad_items", out[1], (nc, d), (users.dtype,), dev)
+    _check(_lib.tt_inbatch_softmax_grad(_ptr(users), _ptr(items), _dtype(users), b, nc, d, float(tau), _ptr(logq),
+                                        _ptr(item_ids), _ptr(valid), _ptr(lse), _ptr(loss), _ptr(grad_loss),
+                                        _ptr(grad_mean), _ptr(out[0]), _ptr(out[1]), _ptr(workspace),
+                                        workspace.numel(), _stream(stream)), "tt_inbatch_softmax_grad")
+    if check:
+        _check(_lib.tt_inbatch_softmax_check(_ptr(workspace), _stream(stream)), "tt_inbatch_softmax_grad")
+    return out[0], out[1]
 
 
 def _check_queries(index: Index, queries: torch.Tensor, exclude):

@@ -16,7 +16,7 @@
 // averaged).
 //
 // Kernels, in launch order:
-//   k5_table_clear  (with item ids) empty the open-addressing table
+//   table_clear     (with item ids) empty the open-addressing table
 //   k5_columns      per column: bias nb_j = -log q_j * log2(e) (-inf for an
 //                   invalid column) and item group g_j (the table slot of its
 //                   id, so equal ids <=> equal groups); zero the error word
@@ -54,6 +54,7 @@
 
 #include "tt_device.cuh"
 #include "tt_internal.h"
+#include "tt_softmax.cuh"
 
 namespace tt {
 namespace {
@@ -77,7 +78,6 @@ constexpr float K5_MAX_FLOOR = -1e30f;       // running max before any column (b
 constexpr float K5_SUM_LIMIT = 0x1p64f;      // largest chunk sum taken without raising the max
 constexpr float K5_LOG2E = 1.4426950408889634f;
 constexpr float K5_LN2 = 0.6931471805599453f;
-constexpr unsigned long long K5_EMPTY = 0x8000000000000000ull;  // free table slot
 constexpr int K5_MERGE_THREADS = 256;
 constexpr int K5_BINS = 256;                 // sort bins: the top 8 bits of the id's hash
 constexpr int K5_SORT_THREADS = 256;         // one element per thread and round
@@ -127,45 +127,6 @@ struct K5Params {
     uint32_t idesc;
 };
 
-// Packed fp32 pairs (sm_100 f32x2): two lanes of work per instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
-// Keep the compiler from moving uses of TMEM-loaded registers above the
-// tcgen05.wait::ld that makes them valid.
-__device__ __forceinline__ void fence_regs(Cols32& c) {
-    asm volatile(""
-                 : "+f"(c.x[0]), "+f"(c.x[1]), "+f"(c.x[2]), "+f"(c.x[3]), "+f"(c.x[4]), "+f"(c.x[5]),
-                   "+f"(c.x[6]), "+f"(c.x[7]), "+f"(c.x[8]), "+f"(c.x[9]), "+f"(c.x[10]), "+f"(c.x[11]),
-                   "+f"(c.x[12]), "+f"(c.x[13]), "+f"(c.x[14]), "+f"(c.x[15]), "+f"(c.x[16]), "+f"(c.x[17]),
-                   "+f"(c.x[18]), "+f"(c.x[19]), "+f"(c.x[20]), "+f"(c.x[21]), "+f"(c.x[22]), "+f"(c.x[23]),
-                   "+f"(c.x[24]), "+f"(c.x[25]), "+f"(c.x[26]), "+f"(c.x[27]), "+f"(c.x[28]), "+f"(c.x[29]),
-                   "+f"(c.x[30]), "+f"(c.x[31]));
-}
-
-__device__ __forceinline__ float ex2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Column j's (bias bits, group); past nc: bias -inf and a group no row has.
 __device__ __forceinline__ int2 load_col(const K5Params& p, int j) {
     if (j < p.nc) return __ldg(reinterpret_cast<const int2*>(p.col) + j);
@@ -182,18 +143,6 @@ __device__ __forceinline__ void unit_cols(const K5Params& p, int u, int* ut, int
 // ---------------------------------------------------------------------------
 // column preparation
 // ---------------------------------------------------------------------------
-__global__ void k5_table_clear(unsigned long long* keys, int64_t slots) {
-    for (int64_t t = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; t < slots;
-         t += (int64_t)gridDim.x * blockDim.x)
-        keys[t] = K5_EMPTY;
-}
-
-// Fibonacci hashing (Knuth, TAOCP vol. 3, 6.4): multiply by 2^64 / golden
-// ratio and keep the top bits.
-__device__ __forceinline__ int64_t k5_hash(unsigned long long id, int log2_slots) {
-    return (int64_t)((id * 0x9E3779B97F4A7C15ull) >> (64 - log2_slots));
-}
-
 __global__ void k5_columns(const float* __restrict__ logq, const uint8_t* __restrict__ valid,
                            const int64_t* __restrict__ item_ids, int nc, unsigned long long* keys,
                            int log2_slots, ColInfo* __restrict__ col, int* err, unsigned* ticket) {
@@ -208,25 +157,7 @@ __global__ void k5_columns(const float* __restrict__ logq, const uint8_t* __rest
     ColInfo c;
     c.nb = ok ? -lq * K5_LOG2E : -INFINITY;
     c.g = 0;
-    if (item_ids) {
-        const unsigned long long id = (unsigned long long)item_ids[j];
-        const int64_t slots = (int64_t)1 << log2_slots;
-        if (id == K5_EMPTY) {
-            c.g = (int)slots;  // the one id the table cannot hold has a group of its own
-        } else {
-            // linear probing; the table has at least twice as many slots as
-            // columns, so a free or matching slot is always found
-            int64_t h = k5_hash(id, log2_slots);
-            for (int64_t probe = 0; probe < slots; ++probe) {
-                const unsigned long long prev = atomicCAS(keys + h, K5_EMPTY, id);
-                if (prev == K5_EMPTY || prev == id) {
-                    c.g = (int)h;
-                    break;
-                }
-                h = (h + 1) & (slots - 1);
-            }
-        }
-    }
+    if (item_ids) c.g = item_group((unsigned long long)item_ids[j], keys, log2_slots);
     col[j] = c;
 }
 
@@ -237,7 +168,7 @@ __global__ void k5_columns(const float* __restrict__ logq, const uint8_t* __rest
 // part 0 = [0, b) (the rows use the same permutation, so row r's positive
 // stays column r) and part 1 = [b, nc) (the shared negatives). The key of
 // column j is bin(id_j), the top 8 bits of the id's Fibonacci hash (as in
-// k5_hash); equal ids share a bin, so the columns that can be
+// table_hash); equal ids share a bin, so the columns that can be
 // hits of row r lie in the column ranges of bin(r) in both parts. Stable
 // ranks make the order, and with it every sum, the same on every run.
 //
@@ -931,7 +862,7 @@ cudaError_t launch_softmax(const SoftmaxPlan& pl, const CUtensorMap& tm_users, c
         const int64_t slots = (int64_t)1 << pl.log2_slots;
         const int blocks = (int)((slots + 255) / 256 < 4 * sm_count ? (slots + 255) / 256 : 4 * sm_count);
         note_launch_begin(TT_KIND_SOFTMAX, s);
-        k5_table_clear<<<blocks, 256, 0, s>>>(keys, slots);
+        table_clear<<<blocks, 256, 0, s>>>(keys, slots);
         note_launch_end(TT_KIND_SOFTMAX, s);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }

@@ -1,0 +1,764 @@
+// k_softmax_grad.cu - K6: the gradient of the in-batch sampled softmax (K5)
+// with respect to the user and item rows, without writing the b x nc matrix.
+//
+// With l_ij = (u_i . v_j) / tau - log q_j, P_ij = exp(l_ij - lse_i) for the
+// columns in row i's sum (0 for the others), and w_i the loss's weight of row
+// i (the gradient of loss_i, plus that of the mean over the valid rows; 0 for
+// padding):
+//   grad_u_i = w_i / tau (sum_j P_ij v_j - v_i)
+//   grad_v_j = 1 / tau (sum_i w_i P_ij u_i - [j < b] w_j u_j)
+// The diagonal is kept out of the matrix products: its coefficient
+// P_ii - 1 = expm1(-loss_i) (both terms of the sums above together) is applied
+// in fp32 at the end, so that the one large entry of a row is not rounded and
+// does not cancel.
+//
+// Kernels, in launch order:
+//   table_clear  (with item ids) empty the table that numbers the ids
+//   k6_prepare   per column: bias -log q_j log2(e), item group; per row:
+//                w_i, -lse_i log2(e) (-inf where w_i = 0), expm1(-loss_i);
+//                with padding, copies of users and items whose padded rows
+//                are zero (what a padded row holds, NaN even, never matters)
+//   k6_products  both gradients' products. One pass keeps 128 users and runs
+//                over the items, the other keeps 128 items and runs over the
+//                users; each forms the logits of a 128 x TN tile again on the
+//                tensor cores, turns them into P in registers, writes P as
+//                bf16 over the logits in tensor memory and multiplies it from
+//                there with the tile of rows that is still in shared memory
+//   k6_finish    adds the partial products of each row, the diagonal, and the
+//                scale, and rounds to bf16
+//
+// P is rounded to bf16 (a relative 2^-9 of each term, of either sign): its
+// products with bf16 rows are then exact and add in fp32, and what the
+// rounding leaves is of the size of the result's own rounding to bf16.
+// Recomputing the logits in both passes costs 2 of the 8 b nc d operations and
+// a second exponential per logit; one pass would need either atomic additions
+// of b x d (or nc x d) sums per tile, whose order changes the result, or
+// their partial sums in HBM.
+//
+// The tiles of both passes, row tile after row tile, form one line that is cut
+// evenly among the SMs, so a few row tiles with long sums use the whole GPU
+// too; the parts of a row tile are added in k6_finish in the order of the
+// line. Every wait is bounded; on expiry the kernel records an error code,
+// every output becomes NaN, and the host check reports a timeout.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "tt_device.cuh"
+#include "tt_internal.h"
+#include "tt_rows.cuh"
+#include "tt_softmax.cuh"
+
+namespace tt {
+namespace {
+
+constexpr int K6_M = 128;            // kept rows per tile (TMEM lanes)
+constexpr int K6_GROUPS = 3;         // groups of four epilogue warps, one tile each in turn
+constexpr int K6_EPI_WARPS = 4 * K6_GROUPS;
+constexpr int K6_THREADS = 32 * (2 + K6_EPI_WARPS);
+constexpr int K6_TMEM_COLS = 512;
+constexpr int K6_MAX_BUFS = 4;       // logit tiles in tensor memory
+constexpr int K6_MAX_STAGES = 8;
+constexpr int K6_SMEM_BUDGET = 227 * 1024;
+constexpr int K6_HALF = 256;         // widest product of one unit; wider rows take two
+constexpr float K6_LOG2E = 1.4426950408889634f;
+constexpr int K6_PREP_THREADS = 256;
+
+template <int TN>
+struct K6Ctl {
+    uint64_t full[K6_MAX_STAGES], empty[K6_MAX_STAGES];
+    uint64_t xfull, xempty;
+    uint64_t sfull[K6_MAX_BUFS];  // logits of a tile are in tensor memory
+    uint64_t pfull[K6_MAX_BUFS];  // P is there in their place
+    uint64_t pdone[K6_MAX_BUFS];  // the product with P is done
+    uint64_t accfull, accempty;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    // per epilogue warp: bias, group and weight of its tile's columns
+    alignas(16) float bias[K6_EPI_WARPS][TN];
+    alignas(16) int grp[K6_EPI_WARPS][TN];
+    alignas(16) float wgt[K6_EPI_WARPS][TN];
+};
+
+struct K6Side {
+    float bias;  // added to acc log2(e) / tau: items -log q log2(e); users -lse log2(e), -inf where w = 0
+    int grp;     // item group
+};
+
+struct K6Params {
+    const K6Side* item;   // [nc]
+    const K6Side* user;   // [b]
+    const float* weight;  // [b] w_i
+    float* part;          // [units + grid][128][width] partial products
+    int* err;
+    int b, nc, d;
+    float a2;             // log2(e) / tau
+    int kchunks;          // 64-element pieces of a row
+    int halves, width;    // products of `width` columns, in `halves` units
+    int stages, bufs, ahead;
+    int64_t work;         // tiles in all
+    uint32_t idesc_s;
+};
+
+// Unit u: half u / (row tiles of both passes), then the users' row tiles, then the items'.
+struct K6Unit {
+    int pass, half, tile, cols;  // cols: tiles of the other side
+    int64_t begin;               // its first tile on the line
+};
+
+template <int TN>
+struct K6Line {
+    int ru, rv;  // row tiles of users, items
+    int cu, cv;  // column tiles of users, items
+    __host__ __device__ K6Line(int b, int nc)
+        : ru((b + K6_M - 1) / K6_M), rv((nc + K6_M - 1) / K6_M), cu((b + TN - 1) / TN), cv((nc + TN - 1) / TN) {}
+    __host__ __device__ int64_t per_half() const { return (int64_t)ru * cv + (int64_t)rv * cu; }
+    __host__ __device__ K6Unit unit(int u) const {
+        K6Unit r;
+        r.half = u / (ru + rv);
+        const int q = u - r.half * (ru + rv);
+        r.pass = q < ru ? 0 : 1;
+        r.tile = r.pass == 0 ? q : q - ru;
+        r.cols = r.pass == 0 ? cv : cu;
+        r.begin = (int64_t)r.half * per_half() + (r.pass == 0 ? (int64_t)r.tile * cv : (int64_t)ru * cv + (int64_t)r.tile * cu);
+        return r;
+    }
+    // the unit that holds tile w of the line
+    __host__ __device__ int unit_of(int64_t w) const {
+        const int half = (int)(w / per_half());
+        const int64_t q = w - (int64_t)half * per_half();
+        const int64_t first = (int64_t)ru * cv;
+        return half * (ru + rv) + (q < first ? (int)(q / cv) : ru + (int)((q - first) / cu));
+    }
+};
+
+__host__ __device__ __forceinline__ int64_t cta_begin(int64_t work, int cta, int grid) {
+    // work * cta may pass 64 bits only beyond 2^53 tiles
+    return work / grid * cta + work % grid * cta / grid;
+}
+
+// ---------------------------------------------------------------------------
+// preparation
+// ---------------------------------------------------------------------------
+struct K6Prep {
+    const float* logq;
+    const int64_t* item_ids;
+    const uint8_t* valid;
+    const float *lse, *loss, *grad_loss, *grad_mean;
+    unsigned long long* keys;
+    int log2_slots;
+    K6Side *item, *user;
+    float *weight, *diag;
+    const uint4 *users, *items;  // copied where valid is given
+    uint4 *users_c, *items_c;
+    int b, nc, vpr;              // vpr: 16-byte pieces of a row
+    int* err;
+};
+
+__global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
+    __shared__ int valid_rows;
+    const int tid = blockIdx.x * K6_PREP_THREADS + threadIdx.x;
+    const int threads = gridDim.x * K6_PREP_THREADS;
+    if (tid == 0) *p.err = 0;
+    if (threadIdx.x == 0) valid_rows = 0;
+    __syncthreads();
+    if (p.valid != nullptr && p.grad_mean != nullptr) {  // every block counts all rows
+        int n = 0;
+        for (int i = threadIdx.x; i < p.b; i += K6_PREP_THREADS) n += p.valid[i] != 0;
+        n = __reduce_add_sync(0xffffffffu, n);
+        if ((threadIdx.x & 31) == 0) atomicAdd(&valid_rows, n);
+        __syncthreads();
+    }
+    const float mean_w = p.grad_mean != nullptr ? *p.grad_mean / (float)(p.valid != nullptr ? valid_rows : p.b) : 0.f;
+    for (int j = tid; j < p.nc; j += threads) {
+        const bool ok = p.valid == nullptr || p.valid[j] != 0;
+        K6Side c;
+        c.bias = ok ? (p.logq != nullptr ? -p.logq[j] * K6_LOG2E : 0.f) : -INFINITY;
+        c.grp = p.item_ids != nullptr ? item_group((unsigned long long)p.item_ids[j], p.keys, p.log2_slots) : 0;
+        p.item[j] = c;
+        if (j < p.b) {
+            const float w = ok ? (p.grad_loss != nullptr ? p.grad_loss[j] : 0.f) + mean_w : 0.f;
+            p.weight[j] = w;
+            p.diag[j] = ok ? expm1f(-p.loss[j]) : 0.f;
+            c.bias = w != 0.f ? -p.lse[j] * K6_LOG2E : -INFINITY;
+            p.user[j] = c;
+        }
+    }
+    if (p.valid == nullptr) return;
+    const int64_t total = (int64_t)p.nc * p.vpr;
+    for (int64_t v = tid; v < total; v += threads) {
+        const int j = (int)(v / p.vpr);
+        const bool ok = p.valid[j] != 0;
+        p.items_c[v] = ok ? __ldg(p.items + v) : make_uint4(0, 0, 0, 0);
+        if (j < p.b) p.users_c[v] = ok ? __ldg(p.users + v) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the products
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+template <int TN, bool HITS>
+__global__ void __launch_bounds__(K6_THREADS, 1)
+    k6_products(const __grid_constant__ CUtensorMap tm_ux, const __grid_constant__ CUtensorMap tm_uy,
+                const __grid_constant__ CUtensorMap tm_vx, const __grid_constant__ CUtensorMap tm_vy,
+                const K6Params p) {
+    constexpr int XCHUNK = K6_M * 128;  // bytes of a 64-element piece of the kept tile
+    constexpr int YCHUNK = TN * 128;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* xsm = smem;                                   // [kchunks][128 x 128 B]
+    uint8_t* ring = smem + (size_t)p.kchunks * XCHUNK;     // [stages][kchunks][TN x 128 B]
+    const int ystage = p.kchunks * YCHUNK;
+    K6Ctl<TN>* ctl = reinterpret_cast<K6Ctl<TN>*>(ring + (size_t)p.stages * ystage);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const K6Line<TN> line(p.b, p.nc);
+    const int64_t w0 = cta_begin(p.work, blockIdx.x, gridDim.x);
+    const int64_t w1 = cta_begin(p.work, blockIdx.x + 1, gridDim.x);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        mbar_init(&ctl->xfull, 1);
+        mbar_init(&ctl->xempty, 1);
+        for (int q = 0; q < p.bufs; ++q) {
+            mbar_init(&ctl->sfull[q], 1);
+            mbar_init(&ctl->pfull[q], 4);
+            mbar_init(&ctl->pdone[q], 1);
+        }
+        mbar_init(&ctl->accfull, 1);
+        mbar_init(&ctl->accempty, K6_EPI_WARPS);
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem_base, K6_TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    const uint32_t acc_cols = (uint32_t)((p.width + 31) / 32 * 32);  // the product; the logit tiles follow
+    volatile int* abort = &ctl->abort;
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        if (lane == 0) {
+            uint32_t n = 0;  // tiles loaded
+            int seg = 0;     // kept tiles loaded
+            bool ok = true;
+            for (int64_t w = w0; ok && w < w1; ++seg) {
+                const K6Unit u = line.unit(line.unit_of(w));
+                const int t0 = (int)(w - u.begin);
+                const int t1 = (int)(u.begin + u.cols < w1 ? u.cols : w1 - u.begin);
+                const CUtensorMap* tx = u.pass == 0 ? &tm_ux : &tm_vx;
+                const CUtensorMap* ty = u.pass == 0 ? &tm_vy : &tm_uy;
+                if (!mbar_wait(&ctl->xempty, (seg & 1) ^ 1, abort)) { ok = false; break; }
+                mbar_arrive_expect_tx(&ctl->xfull, (uint32_t)(p.kchunks * XCHUNK));
+                for (int kc = 0; kc < p.kchunks; ++kc)
+                    tma_load_2d(xsm + (size_t)kc * XCHUNK, tx, &ctl->xfull, kc * 64, u.tile * K6_M);
+                for (int t = t0; t < t1; ++t, ++n) {
+                    const int s = n % p.stages;
+                    if (!mbar_wait(&ctl->empty[s], ((n / p.stages) & 1) ^ 1, abort)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)ystage);
+                    for (int kc = 0; kc < p.kchunks; ++kc)
+                        tma_load_2d(ring + (size_t)s * ystage + (size_t)kc * YCHUNK, ty, &ctl->full[s], kc * 64, t * TN);
+                }
+                w += t1 - t0;
+            }
+            if (!ok) {
+                atomicExch(p.err, ERR_TIMEOUT_TMA);
+                *abort = 1;
+            }
+            // Every issued load must land before the block may exit.
+            const uint32_t first = n > (uint32_t)p.stages ? n - p.stages : 0;
+            for (uint32_t j = first; j < n; ++j) mbar_wait(&ctl->full[j % p.stages], (j / p.stages) & 1, nullptr);
+            if (seg > 0) mbar_wait(&ctl->xfull, (seg - 1) & 1, nullptr);
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        // The logits of tile n + ahead are issued after the product of tile n.
+        // Both walk the line; the walk of the logits is `ahead` tiles in front.
+        if (lane == 0) {
+            const uint32_t xbase = smem_u32(xsm), rbase = smem_u32(ring);
+            bool ok = true;
+            struct Walk {
+                int64_t w;
+                uint32_t n;
+                int seg;
+                int64_t unit_end;
+                bool first, last;
+                K6Unit u;
+            };
+            auto enter = [&](Walk& k) {  // at the first tile of a segment
+                k.u = line.unit(line.unit_of(k.w));
+                k.unit_end = k.u.begin + k.u.cols < w1 ? k.u.begin + k.u.cols : w1;
+                k.first = true;
+            };
+            Walk s, g;
+            s.w = g.w = w0;
+            s.n = g.n = 0;
+            s.seg = g.seg = 0;
+            auto issue_logits = [&]() -> bool {
+                if (s.n == 0 || s.w == s.unit_end) {
+                    if (s.n != 0) ++s.seg;
+                    enter(s);
+                    if (!mbar_wait(&ctl->xfull, s.seg & 1, abort)) return false;
+                }
+                const int st = s.n % p.stages, bf = s.n % p.bufs;
+                if (!mbar_wait(&ctl->pdone[bf], ((s.n / p.bufs) & 1) ^ 1, abort)) return false;
+                if (!mbar_wait(&ctl->full[st], (s.n / p.stages) & 1, abort)) return false;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc_cols + (uint32_t)(bf * TN);
+                for (int kc = 0; kc < p.kchunks; ++kc) {
+                    const uint32_t a = xbase + (uint32_t)(kc * XCHUNK);
+                    const uint32_t b = rbase + (uint32_t)(st * ystage + kc * YCHUNK);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16(d_tmem, umma_desc_kmajor_sw128(a + kk * 32), umma_desc_kmajor_sw128(b + kk * 32),
+                                  p.idesc_s, (kc | kk) != 0 ? 1u : 0u);
+                }
+                umma_commit(&ctl->sfull[bf]);
+                ++s.n;
+                ++s.w;
+                if (s.w == s.unit_end) umma_commit(&ctl->xempty);  // the kept tile is free after this
+                return true;
+            };
+            for (int q = 0; ok && q < p.ahead && s.w < w1; ++q) ok = issue_logits();
+            while (ok && g.w < w1) {
+                if (g.n == 0 || g.w == g.unit_end) {
+                    if (g.n != 0) ++g.seg;
+                    enter(g);
+                    if (!mbar_wait(&ctl->accempty, (g.seg & 1) ^ 1, abort)) { ok = false; break; }
+                }
+                const int st = g.n % p.stages, bf = g.n % p.bufs;
+                if (!mbar_wait(&ctl->pfull[bf], (g.n / p.bufs) & 1, abort)) { ok = false; break; }
+                tc_fence_after();
+                const int cols = p.d - g.u.half * K6_HALF < K6_HALF ? p.d - g.u.half * K6_HALF : K6_HALF;
+                const uint32_t idesc = umma_idesc_bf16_bmn(K6_M, cols);
+                const uint32_t a = tmem_base + acc_cols + (uint32_t)(bf * TN);
+                const uint32_t b = rbase + (uint32_t)(st * ystage + g.u.half * (K6_HALF / 64) * YCHUNK);
+#pragma unroll
+                for (int kk = 0; kk < TN / 16; ++kk)
+                    umma_bf16_ts(tmem_base, a + kk * 8, umma_desc_mnmajor_sw128(b + kk * 2048, YCHUNK), idesc,
+                                 g.first && kk == 0 ? 0u : 1u);
+                g.first = false;
+                umma_commit(&ctl->empty[st]);
+                umma_commit(&ctl->pdone[bf]);
+                ++g.n;
+                ++g.w;
+                if (g.w == g.unit_end) umma_commit(&ctl->accfull);
+                if (s.w < w1) ok = issue_logits();
+            }
+            if (!ok) {
+                atomicExch(p.err, ERR_TIMEOUT_MMA);
+                *abort = 1;
+            }
+            // Wait for every MMA issued by this thread before TMEM is freed.
+            umma_commit(&ctl->drain);
+            mbar_wait(&ctl->drain, 0, nullptr);
+        }
+    } else {
+        // ------------------------------ epilogue ------------------------------
+        // Group g takes tiles g, g + K6_GROUPS, ...; warp w of it TMEM lanes
+        // 32 (w % 4) .., one kept row per thread, all TN columns of the tile.
+        const int ew = warp - 2;
+        const int group = ew >> 2;
+        const int quarter = warp & 3;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        const float2 a2v = make_float2(p.a2, p.a2);
+        float* bias_s = ctl->bias[ew];
+        int* grp_s = ctl->grp[ew];
+        float* wgt_s = ctl->wgt[ew];
+        bool ok = true;
+        uint32_t n = 0;
+        int seg = 0;
+        for (int64_t w = w0; ok && w < w1; ++seg) {
+            const int uid = line.unit_of(w);
+            const K6Unit u = line.unit(uid);
+            const int t0 = (int)(w - u.begin);
+            const int t1 = (int)(u.begin + u.cols < w1 ? u.cols : w1 - u.begin);
+            const int rows = u.pass == 0 ? p.b : p.nc, cols = u.pass == 0 ? p.nc : p.b;
+            const K6Side* xs = u.pass == 0 ? p.user : p.item;
+            const K6Side* ys = u.pass == 0 ? p.item : p.user;
+            const int i = u.tile * K6_M + quarter * 32 + lane;
+            K6Side mine = {-INFINITY, -1};
+            if (i < rows) mine = xs[i];
+            const float2 rowv = make_float2(mine.bias, mine.bias);
+            // first tile of this segment that is this group's
+            int t = t0 + (int)((K6_GROUPS + group - n % K6_GROUPS) % K6_GROUPS);
+            int2 cv[TN / 32];
+            float cw[TN / 32];
+            auto load_cols = [&](int tt) {
+#pragma unroll
+                for (int e = 0; e < TN / 32; ++e) {
+                    const int j = tt * TN + 32 * e + lane;
+                    cv[e] = j < cols ? __ldg(reinterpret_cast<const int2*>(ys) + j) : make_int2((int)0xff800000u, -2);
+                    cw[e] = u.pass == 1 && j < cols ? __ldg(p.weight + j) : 0.f;
+                }
+            };
+            if (t < t1) load_cols(t);
+            for (; t < t1; t += K6_GROUPS) {
+                const uint32_t nt = n + (uint32_t)(t - t0);
+                const int bf = nt % p.bufs;
+                __syncwarp();  // the previous tile's reads are done
+#pragma unroll
+                for (int e = 0; e < TN / 32; ++e) {
+                    bias_s[32 * e + lane] = __int_as_float(cv[e].x);
+                    if (HITS) grp_s[32 * e + lane] = cv[e].y;
+                    if (u.pass == 1) wgt_s[32 * e + lane] = cw[e];
+                }
+                __syncwarp();
+                if (t + K6_GROUPS < t1) load_cols(t + K6_GROUPS);
+                if (!mbar_wait(&ctl->sfull[bf], (nt / p.bufs) & 1, abort)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t buf = lane_base + acc_cols + (uint32_t)(bf * TN);
+#pragma unroll 1
+                for (int c = 0; c < TN / 32; ++c) {
+                    Cols32 v;
+                    tmem_ld_32cols(buf + c * 32, v.x);
+                    tmem_ld_wait();
+                    fence_regs(v);
+                    const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
+                    const int4* g4 = reinterpret_cast<const int4*>(grp_s + c * 32);
+                    const float4* w4 = reinterpret_cast<const float4*>(wgt_s + c * 32);
+#pragma unroll
+                    for (int e4 = 0; e4 < 8; ++e4) {
+                        const float4 bb = b4[e4];
+                        float2 lo = fma2(make_float2(v.x[4 * e4], v.x[4 * e4 + 1]), a2v, make_float2(bb.x, bb.y));
+                        float2 hi = fma2(make_float2(v.x[4 * e4 + 2], v.x[4 * e4 + 3]), a2v, make_float2(bb.z, bb.w));
+                        lo = add2(lo, rowv);
+                        hi = add2(hi, rowv);
+                        if constexpr (HITS) {  // the diagonal among them
+                            const int4 gg = g4[e4];
+                            lo.x = gg.x == mine.grp ? -INFINITY : lo.x;
+                            lo.y = gg.y == mine.grp ? -INFINITY : lo.y;
+                            hi.x = gg.z == mine.grp ? -INFINITY : hi.x;
+                            hi.y = gg.w == mine.grp ? -INFINITY : hi.y;
+                        }
+                        v.x[4 * e4] = lo.x;
+                        v.x[4 * e4 + 1] = lo.y;
+                        v.x[4 * e4 + 2] = hi.x;
+                        v.x[4 * e4 + 3] = hi.y;
+                    }
+                    if constexpr (!HITS) {
+                        const int at = i - (t * TN + c * 32);
+                        if ((unsigned)at < 32u) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v.x[e] = e == at ? -INFINITY : v.x[e];
+                        }
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e4 = 0; e4 < 8; ++e4) {
+                        float2 lo = make_float2(ex2_approx(v.x[4 * e4]), ex2_approx(v.x[4 * e4 + 1]));
+                        float2 hi = make_float2(ex2_approx(v.x[4 * e4 + 2]), ex2_approx(v.x[4 * e4 + 3]));
+                        if (u.pass == 1) {
+                            const float4 ww = w4[e4];
+                            lo = mul2(lo, make_float2(ww.x, ww.y));
+                            hi = mul2(hi, make_float2(ww.z, ww.w));
+                        }
+                        pk[2 * e4] = bf16x2_bits(lo.x, lo.y);
+                        pk[2 * e4 + 1] = bf16x2_bits(hi.x, hi.y);
+                    }
+                    // P of chunk c covers logits that this thread has read already
+                    tmem_st_16cols(buf + c * 16, pk);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->pfull[bf]);
+            }
+            if (!ok) break;
+            // the product of this segment
+            if (!mbar_wait(&ctl->accfull, seg & 1, abort)) { ok = false; break; }
+            tc_fence_after();
+            const int width = p.d - u.half * K6_HALF < K6_HALF ? p.d - u.half * K6_HALF : K6_HALF;
+            float* out = p.part + ((int64_t)(uid + blockIdx.x) * K6_M + quarter * 32 + lane) * p.width;
+            for (int c = group * 32; c < width; c += K6_GROUPS * 32) {
+                Cols32 v;
+                tmem_ld_32cols(lane_base + c, v.x);
+                tmem_ld_wait();
+                fence_regs(v);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    if (c + e < width)
+                        *reinterpret_cast<float4*>(out + c + e) = make_float4(v.x[e], v.x[e + 1], v.x[e + 2], v.x[e + 3]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->accempty);
+            n += (uint32_t)(t1 - t0);
+            w += t1 - t0;
+        }
+        if (!ok) {
+            atomicExch(p.err, ERR_TIMEOUT_EPI);
+            *abort = 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, K6_TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the sums of the parts, the diagonal, the scale
+// ---------------------------------------------------------------------------
+struct K6Finish {
+    const float* part;
+    const float *weight, *diag;  // [b]
+    const __nv_bfloat16 *users, *items;
+    __nv_bfloat16 *grad_users, *grad_items;
+    const int* err;
+    int b, nc, d, halves, width, grid;
+    int64_t work;
+    float inv_tau;
+};
+
+// A thread takes 8 columns of a row: of the users, then of the items.
+template <int TN>
+__global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
+    const K6Line<TN> line(p.b, p.nc);
+    const int vpr = p.d / 8;
+    const int64_t total = ((int64_t)p.b + p.nc) * vpr;
+    const bool failed = *p.err != 0;
+    for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < total; v += (int64_t)gridDim.x * 256) {
+        const int64_t r = v / vpr;
+        const int col = (int)(v - r * vpr) * 8;
+        const int pass = r < p.b ? 0 : 1;
+        const int i = pass == 0 ? (int)r : (int)(r - p.b);
+        const int half = col / K6_HALF;
+        const int uid = half * (line.ru + line.rv) + (pass == 0 ? 0 : line.ru) + i / K6_M;
+        const K6Unit u = line.unit(uid);
+        // the blocks whose stretch of the line meets the unit's
+        int c = (int)((u.begin * p.grid) / p.work);
+        while (c > 0 && cta_begin(p.work, c, p.grid) > u.begin) --c;
+        while (cta_begin(p.work, c + 1, p.grid) <= u.begin) ++c;
+        float acc[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+        for (; c < p.grid && cta_begin(p.work, c, p.grid) < u.begin + u.cols; ++c) {
+            const float4* q = reinterpret_cast<const float4*>(
+                p.part + ((int64_t)(uid + c) * K6_M + i % K6_M) * p.width + (col - half * K6_HALF));
+            const float4 x = __ldg(q), y = __ldg(q + 1);
+            acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
+            acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
+        }
+        const float w = i < p.b ? p.weight[i] : 0.f;
+        float out[8];
+        if (w != 0.f) {
+            Raw<__nv_bfloat16, 8> other;
+            float x[8];
+            other.load((pass == 0 ? p.items : p.users) + (int64_t)i * p.d + col);
+            other.get(x);
+            const float c_ii = p.diag[i];
+            if (pass == 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) out[k] = fmaf(c_ii, x[k], acc[k]) * w * p.inv_tau;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) out[k] = fmaf(c_ii * w, x[k], acc[k]) * p.inv_tau;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) out[k] = pass == 0 ? 0.f : acc[k] * p.inv_tau;
+        }
+        if (failed) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) out[k] = NAN;
+        }
+        store_row<8>((pass == 0 ? p.grad_users : p.grad_items) + (int64_t)i * p.d + col, out);
+    }
+}
+
+int log2_ceil(int64_t x) {
+    int l = 0;
+    while (((int64_t)1 << l) < x) ++l;
+    return l;
+}
+
+template <int TN>
+int stages_for(int kchunks) {
+    const int fixed = 1024 + kchunks * K6_M * 128 + (int)sizeof(K6Ctl<TN>);
+    const int s = (K6_SMEM_BUDGET - fixed) / (kchunks * TN * 128);
+    return s < K6_MAX_STAGES ? s : K6_MAX_STAGES;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+SoftmaxGradPlan softmax_grad_plan(int b, int nc, int d, bool item_ids, bool copies, int sm_count) {
+    SoftmaxGradPlan pl;
+    const int kchunks = (d + 63) / 64;
+    pl.tile_cols = d <= 128 ? 128 : 64;
+    pl.halves = (d + K6_HALF - 1) / K6_HALF;
+    pl.width = d < K6_HALF ? d : K6_HALF;
+    const int acc = (pl.width + 31) / 32 * 32;
+    pl.bufs = (K6_TMEM_COLS - acc) / pl.tile_cols;
+    if (pl.bufs > K6_MAX_BUFS) pl.bufs = K6_MAX_BUFS;
+    pl.stages = pl.tile_cols == 128 ? stages_for<128>(kchunks) : stages_for<64>(kchunks);
+    pl.ahead = pl.bufs - 1 < pl.stages ? pl.bufs - 1 : pl.stages;
+    int64_t units;
+    if (pl.tile_cols == 128) {
+        const K6Line<128> line(b, nc);
+        pl.work = line.per_half() * pl.halves;
+        units = (int64_t)(line.ru + line.rv) * pl.halves;
+    } else {
+        const K6Line<64> line(b, nc);
+        pl.work = line.per_half() * pl.halves;
+        units = (int64_t)(line.ru + line.rv) * pl.halves;
+    }
+    pl.grid = pl.work < sm_count ? (int)pl.work : sm_count;
+    pl.log2_slots = item_ids ? log2_ceil(2 * (int64_t)(nc > 32 ? nc : 32)) : 0;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    pl.off_err = take(sizeof(int));  // first: tt_inbatch_softmax_check reads it at offset 0
+    pl.off_item = take((size_t)nc * sizeof(K6Side));
+    pl.off_user = take((size_t)b * sizeof(K6Side));
+    pl.off_weight = take((size_t)b * sizeof(float));
+    pl.off_diag = take((size_t)b * sizeof(float));
+    pl.off_keys = take(item_ids ? ((size_t)1 << pl.log2_slots) * sizeof(unsigned long long) : 0);
+    pl.off_users_c = take(copies ? (size_t)b * d * 2 : 0);
+    pl.off_items_c = take(copies ? (size_t)nc * d * 2 : 0);
+    pl.off_part = take((size_t)(units + pl.grid) * K6_M * pl.width * sizeof(float));
+    pl.bytes = off;
+    return pl;
+}
+
+namespace {
+
+template <int TN, bool HITS>
+cudaError_t launch_products(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, const K6Params& p, cudaStream_t s) {
+    const int smem = 1024 + p.kchunks * K6_M * 128 + p.stages * p.kchunks * TN * 128 + (int)sizeof(K6Ctl<TN>);
+    cudaError_t e = cudaFuncSetAttribute(k6_products<TN, HITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
+    k6_products<TN, HITS><<<pl.grid, K6_THREADS, smem, s>>>(g.tm_ux, g.tm_uy, g.tm_vx, g.tm_vy, p);
+    note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
+    return cudaGetLastError();
+}
+
+template <int TN>
+cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStream_t s, int sm_count) {
+    uint8_t* ws = static_cast<uint8_t*>(g.workspace);
+    const bool hits = g.item_ids != nullptr;
+    cudaError_t e;
+    unsigned long long* keys = reinterpret_cast<unsigned long long*>(ws + pl.off_keys);
+    if (hits) {
+        const int64_t slots = (int64_t)1 << pl.log2_slots;
+        const int64_t blocks = (slots + 255) / 256;
+        note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
+        table_clear<<<(int)(blocks < 4 * sm_count ? blocks : 4 * sm_count), 256, 0, s>>>(keys, slots);
+        note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    K6Prep q;
+    q.logq = g.logq;
+    q.item_ids = g.item_ids;
+    q.valid = g.valid;
+    q.lse = g.lse;
+    q.loss = g.loss;
+    q.grad_loss = g.grad_loss;
+    q.grad_mean = g.grad_mean;
+    q.keys = keys;
+    q.log2_slots = pl.log2_slots;
+    q.item = reinterpret_cast<K6Side*>(ws + pl.off_item);
+    q.user = reinterpret_cast<K6Side*>(ws + pl.off_user);
+    q.weight = reinterpret_cast<float*>(ws + pl.off_weight);
+    q.diag = reinterpret_cast<float*>(ws + pl.off_diag);
+    q.users = static_cast<const uint4*>(g.users);
+    q.items = static_cast<const uint4*>(g.items);
+    q.users_c = reinterpret_cast<uint4*>(ws + pl.off_users_c);
+    q.items_c = reinterpret_cast<uint4*>(ws + pl.off_items_c);
+    q.b = g.b;
+    q.nc = g.nc;
+    q.vpr = g.d / 8;
+    q.err = reinterpret_cast<int*>(ws + pl.off_err);
+    const int64_t prep = ((int64_t)g.nc + K6_PREP_THREADS - 1) / K6_PREP_THREADS;
+    note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
+    k6_prepare<<<(int)(prep < 4 * sm_count ? prep : 4 * sm_count), K6_PREP_THREADS, 0, s>>>(q);
+    note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+    K6Params p;
+    p.item = q.item;
+    p.user = q.user;
+    p.weight = q.weight;
+    p.part = reinterpret_cast<float*>(ws + pl.off_part);
+    p.err = q.err;
+    p.b = g.b;
+    p.nc = g.nc;
+    p.d = g.d;
+    p.a2 = (float)(1.4426950408889634 / (double)g.tau);
+    p.kchunks = (g.d + 63) / 64;
+    p.halves = pl.halves;
+    p.width = pl.width;
+    p.stages = pl.stages;
+    p.bufs = pl.bufs;
+    p.ahead = pl.ahead;
+    p.work = pl.work;
+    p.idesc_s = umma_idesc_bf16(K6_M, TN);
+    e = hits ? launch_products<TN, true>(pl, g, p, s) : launch_products<TN, false>(pl, g, p, s);
+    if (e != cudaSuccess) return e;
+
+    K6Finish f;
+    f.part = p.part;
+    f.weight = q.weight;
+    f.diag = q.diag;
+    const bool copies = g.valid != nullptr;
+    f.users = static_cast<const __nv_bfloat16*>(copies ? static_cast<const void*>(q.users_c) : g.users);
+    f.items = static_cast<const __nv_bfloat16*>(copies ? static_cast<const void*>(q.items_c) : g.items);
+    f.grad_users = static_cast<__nv_bfloat16*>(g.grad_users);
+    f.grad_items = static_cast<__nv_bfloat16*>(g.grad_items);
+    f.err = q.err;
+    f.b = g.b;
+    f.nc = g.nc;
+    f.d = g.d;
+    f.halves = pl.halves;
+    f.width = pl.width;
+    f.grid = pl.grid;
+    f.work = pl.work;
+    f.inv_tau = (float)(1.0 / (double)g.tau);
+    const int64_t blocks = (((int64_t)g.b + g.nc) * (g.d / 8) + 255) / 256;
+    note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
+    k6_finish<TN><<<(int)(blocks < 16 * sm_count ? blocks : 16 * sm_count), 256, 0, s>>>(f);
+    note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_softmax_grad(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStream_t s, int sm_count) {
+    return pl.tile_cols == 128 ? launch_all<128>(pl, g, s, sm_count) : launch_all<64>(pl, g, s, sm_count);
+}
+
+}  // namespace tt

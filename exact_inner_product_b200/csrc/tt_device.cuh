@@ -209,6 +209,18 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulation: lane m of A's
+// columns holds row m, two consecutive elements of K per 32-bit column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, signed int8 inputs, exact int32
 // accumulation (K = 32 per instruction).
 __device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -253,6 +265,19 @@ __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// 16 consecutive 32-bit columns of this thread's TMEM lane, and the wait that
+// completes the thread's earlier stores.
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // Shared-memory matrix descriptor for a K-major bf16 operand laid out by a
 // 128-byte-swizzled TMA box: rows of 128 bytes (64 bf16 of K), 8-row groups
 // 1024 bytes apart. start: byte address in shared memory (the tile base must
@@ -267,6 +292,20 @@ __device__ __forceinline__ uint64_t umma_desc_kmajor_sw128(uint32_t start) {
     return desc;
 }
 
+// The same TMA box read as an MN-major operand: its rows run along K, its 64
+// elements per row along N. Blocks of 64 elements of N lie `block_bytes` apart
+// (one box each), groups of 8 rows of K 1024 bytes; K steps of 16 advance
+// start by 2048.
+__device__ __forceinline__ uint64_t umma_desc_mnmajor_sw128(uint32_t start, uint32_t block_bytes) {
+    uint64_t desc = 0;
+    desc |= (uint64_t)((start >> 4) & 0x3FFFu);              // start address, bits 0-13
+    desc |= (uint64_t)((block_bytes >> 4) & 0x3FFFu) << 16;  // leading byte offset: next 64 elements of N
+    desc |= (uint64_t)(1024u >> 4) << 32;                    // stride byte offset: next 8 rows of K
+    desc |= (uint64_t)1u << 46;                              // descriptor version (sm_100)
+    desc |= (uint64_t)2u << 61;                              // layout: 128-byte swizzle
+    return desc;
+}
+
 // Instruction descriptor: kind::f16 with bf16 A and B (both K-major), fp32
 // accumulator, shape M x N.
 __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n) {
@@ -276,6 +315,9 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int m, int n) {
            | ((uint32_t)(n >> 3) << 17)       // N / 8
            | ((uint32_t)(m >> 4) << 24);      // M / 16
 }
+
+// The same with B MN-major.
+__host__ __device__ constexpr uint32_t umma_idesc_bf16_bmn(int m, int n) { return umma_idesc_bf16(m, n) | (1u << 16); }
 
 // Instruction descriptor: kind::i8 with signed int8 A and B (both K-major),
 // int32 accumulator, shape M x N.

@@ -305,4 +305,29 @@ struct EmbeddingGrad {
 size_t embedding_grad_bytes(int64_t m, int64_t rows, int d);
 cudaError_t launch_embedding_grad(const EmbeddingGrad& g, bool by_row, cudaStream_t s, int sm_count);
 
+// The gradient of the in-batch softmax (k_softmax_grad.cu): work split and
+// workspace layout (the error word is at offset 0).
+struct SoftmaxGradPlan {
+    int tile_cols, halves, width, bufs, stages, ahead, grid, log2_slots;
+    int64_t work;
+    size_t off_err, off_item, off_user, off_weight, off_diag, off_keys, off_users_c, off_items_c, off_part;
+    size_t bytes;
+};
+// copies: padding is given, so that the products read copies of the rows with
+// zeros in the padded ones (off_users_c, off_items_c).
+SoftmaxGradPlan softmax_grad_plan(int b, int nc, int d, bool item_ids, bool copies, int sm_count);
+struct SoftmaxGrad {
+    // rows as boxes of 64 elements x 128 rows (kept tiles), x tile_cols rows (tiles run over)
+    CUtensorMap tm_ux, tm_uy, tm_vx, tm_vy;
+    const void *users, *items;
+    int b, nc, d;
+    float tau;
+    const float* logq;
+    const int64_t* item_ids;
+    const uint8_t* valid;
+    const float *lse, *loss, *grad_loss, *grad_mean;
+    void *grad_users, *grad_items, *workspace;
+};
+cudaError_t launch_softmax_grad(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStream_t s, int sm_count);
+
 }  // namespace tt

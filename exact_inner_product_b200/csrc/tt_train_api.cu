@@ -6,11 +6,18 @@
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
+#include <string.h>
 
 #include <algorithm>
 
 #include "../../include/tt.h"
 #include "tt_internal.h"
+
+#define TT_CUDA(call, what)                                \
+    do {                                                   \
+        const cudaError_t _e = (call);                     \
+        if (_e != cudaSuccess) return cuda_fail(_e, what); \
+    } while (0)
 
 namespace tt {
 namespace {
@@ -333,6 +340,90 @@ tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64_t m, c
     return embedding_grad({ids, id_bytes, m, rows, grad, grad_dtype, d, scale, out_rows, out_dtype, out_ids, count,
                            workspace},
                           true, workspace_bytes, stream);
+}
+
+static tt_status softmax_grad_sizes(int32_t b, int32_t nc, int32_t d, bool with_ids) {
+    if (b < 0 || nc < b || d <= 0) return TT_ERR_INVALID_ARG;
+    if (d % 16 != 0 || d < 64 || d > TT_MAX_D) return TT_ERR_UNSUPPORTED;
+    if (with_ids && nc > (1 << 28)) return TT_ERR_UNSUPPORTED;
+    return TT_OK;
+}
+
+tt_status tt_inbatch_softmax_grad_workspace(int32_t b, int32_t nc, int32_t d, int32_t with_item_ids,
+                                            int32_t with_valid, size_t* bytes) {
+    if (bytes == nullptr) return TT_ERR_INVALID_ARG;
+    const tt_status st = softmax_grad_sizes(b, nc, d, with_item_ids != 0);
+    if (st != TT_OK) return st;
+    *bytes = softmax_grad_plan(b, nc, d, with_item_ids != 0, with_valid != 0, sm_count_current()).bytes;
+    return TT_OK;
+}
+
+tt_status tt_inbatch_softmax_grad(const void* users, const void* items, tt_dtype dtype, int32_t b, int32_t nc,
+                                  int32_t d, float tau, const float* logq, const int64_t* item_ids,
+                                  const uint8_t* valid, const float* lse, const float* loss, const float* grad_loss,
+                                  const float* grad_mean, void* grad_users, void* grad_items, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    if (dtype != TT_BF16) return dtype == TT_F32 || dtype == TT_I8 ? TT_ERR_UNSUPPORTED : TT_ERR_INVALID_ARG;
+    tt_status st = softmax_grad_sizes(b, nc, d, item_ids != nullptr);
+    if (st != TT_OK) return st;
+    if (!(tau > 0.0f) || !isfinite(tau)) return TT_ERR_INVALID_ARG;
+    if (grad_loss == nullptr && grad_mean == nullptr) return TT_ERR_INVALID_ARG;
+    if (b > 0 && (users == nullptr || lse == nullptr || loss == nullptr || grad_users == nullptr)) return TT_ERR_INVALID_ARG;
+    if (nc > 0 && (items == nullptr || grad_items == nullptr)) return TT_ERR_INVALID_ARG;
+    if (!aligned(users, 16) || !aligned(items, 16) || !aligned(grad_users, 16) || !aligned(grad_items, 16) ||
+        !aligned(logq, 4) || !aligned(item_ids, 8) || !aligned(lse, 4) || !aligned(loss, 4) || !aligned(grad_loss, 4) ||
+        !aligned(grad_mean, 4))
+        return TT_ERR_INVALID_ARG;
+    const int sms = sm_count_current();
+    const SoftmaxGradPlan pl = softmax_grad_plan(b, nc, d, item_ids != nullptr, valid != nullptr, sms);
+    if ((st = check_workspace(workspace, workspace_bytes, pl.bytes)) != TT_OK) return st;
+    const size_t u_bytes = (size_t)b * d * 2, v_bytes = (size_t)nc * d * 2;
+    Buffers k;
+    k.in(users, u_bytes, "users");
+    k.in(items, v_bytes, "items");
+    k.in(logq, nc * sizeof(float), "logq");
+    k.in(item_ids, nc * sizeof(int64_t), "item_ids");
+    k.in(valid, nc, "valid");
+    k.in(lse, b * sizeof(float), "lse");
+    k.in(loss, b * sizeof(float), "loss");
+    k.in(grad_loss, b * sizeof(float), "grad_loss");
+    k.in(grad_mean, sizeof(float), "grad_mean");
+    k.out(grad_users, u_bytes, "grad_users");
+    k.out(grad_items, v_bytes, "grad_items");
+    k.out(workspace, pl.bytes, "workspace");
+    if ((st = k.check()) != TT_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (b == 0) {  // no rows: no sums; the error word says that nothing failed
+        TT_CUDA(cudaMemsetAsync(workspace, 0, sizeof(int), s), "error word");
+        if (nc > 0) TT_CUDA(cudaMemsetAsync(grad_items, 0, v_bytes, s), "item gradients");
+        return TT_OK;
+    }
+    SoftmaxGrad g;
+    memset(&g, 0, sizeof g);
+    const uint8_t* ws = static_cast<const uint8_t*>(workspace);
+    const void* u_src = valid != nullptr ? ws + pl.off_users_c : users;
+    const void* v_src = valid != nullptr ? ws + pl.off_items_c : items;
+    if (!bf16_tile_tensor_map(u_src, b, d, d, 128, &g.tm_ux) || !bf16_tile_tensor_map(u_src, b, d, d, pl.tile_cols, &g.tm_uy) ||
+        !bf16_tile_tensor_map(v_src, nc, d, d, 128, &g.tm_vx) || !bf16_tile_tensor_map(v_src, nc, d, d, pl.tile_cols, &g.tm_vy))
+        return TT_ERR_CUDA;
+    g.users = users;
+    g.items = items;
+    g.b = b;
+    g.nc = nc;
+    g.d = d;
+    g.tau = tau;
+    g.logq = logq;
+    g.item_ids = item_ids;
+    g.valid = valid;
+    g.lse = lse;
+    g.loss = loss;
+    g.grad_loss = grad_loss;
+    g.grad_mean = grad_mean;
+    g.grad_users = grad_users;
+    g.grad_items = grad_items;
+    g.workspace = workspace;
+    const cudaError_t e = launch_softmax_grad(pl, g, s, sms);
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "in-batch softmax gradient");
 }
 
 }  // extern "C"

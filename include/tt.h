@@ -410,8 +410,8 @@ TT_API tt_status tt_inbatch_softmax(const void* users, const void* items, tt_dty
                                     int32_t d, float tau, const float* logq, const int64_t* item_ids,
                                     const uint8_t* valid, float* lse, float* loss, float* mean, void* workspace,
                                     size_t workspace_bytes, void* stream);
-/* Wait for the last tt_inbatch_softmax that used `workspace` (on `stream`)
- * and report TT_OK or TT_ERR_TIMEOUT. */
+/* Wait for the last tt_inbatch_softmax or tt_inbatch_softmax_grad that used
+ * `workspace` (on `stream`) and report TT_OK or TT_ERR_TIMEOUT. */
 TT_API tt_status tt_inbatch_softmax_check(const void* workspace, void* stream);
 
 /* ---------------------------------------------------------------------------
@@ -567,6 +567,42 @@ TT_API tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64
                                         void* out_rows, tt_dtype out_dtype, int32_t* count, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
+/*
+ * tt_inbatch_softmax_grad - the gradient of tt_inbatch_softmax with respect to
+ * the user and item rows, without writing the b x nc matrix.
+ *
+ *   P_ij = exp(l_ij - lse_i) for the columns in row i's denominator, else 0
+ *   w_i  = grad_loss_i + grad_mean / (number of valid rows) for valid rows, else 0
+ *   grad_users_i = w_i / tau (sum_j P_ij v_j - v_i)
+ *   grad_items_j = 1 / tau (sum_i w_i P_ij u_i - w_j u_j)   (the last term for j < b)
+ *
+ * The logits are formed as in the loss; P enters the products rounded to bf16
+ * (the diagonal apart, which is added in fp32), the sums are fp32, and the
+ * results are rounded to bf16. Rows of padding, users and items, get zero
+ * gradients, and what they hold (NaN too) changes nothing. (The loss itself
+ * needs finite item rows, padding included.)
+ *
+ * users, items, dtype, b, nc, d, tau, logq, item_ids, valid
+ *             as for tt_inbatch_softmax, and the same values
+ * lse, loss   device f32 [b]: what tt_inbatch_softmax wrote
+ * grad_loss   device f32 [b], the gradient of loss, or NULL for zeros
+ * grad_mean   device f32 [1], the gradient of mean, or NULL for zero
+ *             (not both NULL)
+ * grad_users  device bf16 [b, d]
+ * grad_items  device bf16 [nc, d]
+ * workspace   tt_inbatch_softmax_grad_workspace bytes
+ *
+ * A device-side timeout is reported as for tt_inbatch_softmax: NaN in every
+ * output, and TT_ERR_TIMEOUT from tt_inbatch_softmax_check(workspace).
+ */
+TT_API tt_status tt_inbatch_softmax_grad_workspace(int32_t b, int32_t nc, int32_t d, int32_t with_item_ids,
+                                                   int32_t with_valid, size_t* bytes);
+TT_API tt_status tt_inbatch_softmax_grad(const void* users, const void* items, tt_dtype dtype, int32_t b, int32_t nc,
+                                         int32_t d, float tau, const float* logq, const int64_t* item_ids,
+                                         const uint8_t* valid, const float* lse, const float* loss,
+                                         const float* grad_loss, const float* grad_mean, void* grad_users,
+                                         void* grad_items, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Release a handle. Its work memory returns to a per-device pool that later
  * handles reuse (it is not returned to CUDA before the process exits); a
  * later user's stream first waits for the work this handle had enqueued, so
@@ -629,7 +665,8 @@ TT_API tt_status tt_score_topk_noalloc(const void* rows, tt_dtype dtype, int64_t
 #define TT_KIND_ROWNORM 8  /* layer norm, and the gradients of the row norms */
 #define TT_KIND_CLIP 9     /* the global norm and clipping */
 #define TT_KIND_EMBEDDING 10 /* embedding lookup and its gradient */
-#define TT_NUM_KINDS 11
+#define TT_KIND_SOFTMAX_GRAD 11 /* tt_inbatch_softmax_grad */
+#define TT_NUM_KINDS 12
 
 /* Total kernels this library has launched in the process. */
 TT_API int64_t tt_launch_count(void);

@@ -131,3 +131,31 @@ def test_embedding_grad_arguments():
         assert call(ws=None) == INV and call(ws=ODD) == INV and call(size=need - 1) == INV
         assert call(out=P[1]) == INV and call(ws=P[1]) == INV
     assert by_row(oids=None) == INV and by_row(count=None) == INV and by_row(oids=P[0]) == INV and by_row(count=P[2]) == INV
+
+
+def test_inbatch_softmax_grad_arguments():
+    size = ctypes.c_size_t(0)
+    need_of = tt._lib.tt_inbatch_softmax_grad_workspace
+    assert need_of(8, 9, 64, 1, 1, None) == INV
+    assert need_of(9, 8, 64, 1, 1, ctypes.byref(size)) == INV and need_of(-1, 8, 64, 1, 1, ctypes.byref(size)) == INV
+    assert need_of(8, 9, 72, 1, 1, ctypes.byref(size)) == UNS and need_of(8, 9, 48, 1, 1, ctypes.byref(size)) == UNS
+    assert need_of(8, 9, 528, 1, 1, ctypes.byref(size)) == UNS
+    assert need_of(8, (1 << 28) + 1, 64, 1, 1, ctypes.byref(size)) == UNS
+    assert need_of(8, 9, 64, 1, 1, ctypes.byref(size)) == tt.TT_OK
+    need = size.value
+
+    def call(u=P[0], v=P[1], dt=tt.TT_BF16, b=8, nc=9, d=64, tau=0.1, logq=P[2], ids=P[3], valid=P[4], lse=P[5], loss=P[6],
+             gl=P[7], gm=P[8], gu=P[9], gv=P[10], ws=P[11], size=need):
+        return tt._lib.tt_inbatch_softmax_grad(u, v, dt, b, nc, d, tau, logq, ids, valid, lse, loss, gl, gm, gu, gv, ws, size,
+                                               None)
+
+    assert call(dt=tt.TT_F32) == UNS and call(dt=7) == INV
+    assert call(b=10) == INV and call(b=-1) == INV and call(d=0) == INV and call(d=72) == UNS and call(d=48) == UNS
+    assert call(tau=0.0) == INV and call(tau=-1.0) == INV and call(tau=float("nan")) == INV and call(tau=float("inf")) == INV
+    assert call(gl=None, gm=None) == INV
+    for name in ("u", "v", "lse", "loss", "gu", "gv", "ws"):
+        assert call(**{name: None}) == INV, name
+    for name in ("u", "v", "ids", "lse", "loss", "gl", "gm", "gu", "gv", "ws", "logq"):
+        assert call(**{name: ctypes.c_void_p(0x1000001)}) == INV, name
+    assert call(size=need - 1) == INV
+    assert call(gu=P[0]) == INV and call(gv=P[1]) == INV and call(gv=P[9]) == INV and call(ws=P[5]) == INV
