@@ -58,7 +58,7 @@ namespace {
 constexpr int K6_M = 128;            // kept rows per tile (TMEM lanes)
 constexpr int K6_GROUPS = 3;         // groups of four epilogue warps, one tile each in turn
 constexpr int K6_EPI_WARPS = 4 * K6_GROUPS;
-constexpr int K6_THREADS = 32 * (2 + K6_EPI_WARPS);
+constexpr int K6_THREADS = 32 * (3 + K6_EPI_WARPS);
 constexpr int K6_TMEM_COLS = 512;
 constexpr int K6_MAX_BUFS = 4;       // logit tiles in tensor memory
 constexpr int K6_MAX_STAGES = 8;
@@ -75,7 +75,7 @@ struct K6Ctl {
     uint64_t pfull[K6_MAX_BUFS];  // P is there in their place
     uint64_t pdone[K6_MAX_BUFS];  // the product with P is done
     uint64_t accfull, accempty;
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
     // per epilogue warp: bias, group and weight of its tile's columns
@@ -99,7 +99,7 @@ struct K6Params {
     float a2;             // log2(e) / tau
     int kchunks;          // 64-element pieces of a row
     int halves, width;    // products of `width` columns, in `halves` units
-    int stages, bufs, ahead;
+    int stages, bufs;
     int64_t work;         // tiles in all
     uint32_t idesc_s;
 };
@@ -211,6 +211,24 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return d;
 }
 
+// A place in a ring of buffers and the parity of its current round.
+struct Ring {
+    int at, len;
+    uint32_t phase;
+    __device__ __forceinline__ explicit Ring(int n) : at(0), len(n), phase(0) {}
+    __device__ __forceinline__ void next() {
+        if (++at == len) {
+            at = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <int P>
+struct Pass {
+    static constexpr int value = P;
+};
+
 template <int TN, bool HITS>
 __global__ void __launch_bounds__(K6_THREADS, 1)
     k6_products(const __grid_constant__ CUtensorMap tm_ux, const __grid_constant__ CUtensorMap tm_uy,
@@ -245,7 +263,8 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
         }
         mbar_init(&ctl->accfull, 1);
         mbar_init(&ctl->accempty, K6_EPI_WARPS);
-        mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->drain[0], 1);
+        mbar_init(&ctl->drain[1], 1);
         ctl->abort = 0;
         fence_barrier_init();
     }
@@ -295,87 +314,85 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
             if (seg > 0) mbar_wait(&ctl->xfull, (seg - 1) & 1, nullptr);
         }
     } else if (warp == 1) {
-        // ------------------------------ MMA issuer ------------------------------
-        // The logits of tile n + ahead are issued after the product of tile n.
-        // Both walk the line; the walk of the logits is `ahead` tiles in front.
+        // ------------------------------ logits ------------------------------
+        // One thread issues the logits of every tile, as soon as its buffer (the
+        // product of the tile that had it before) and its stage are there.
         if (lane == 0) {
-            const uint32_t xbase = smem_u32(xsm), rbase = smem_u32(ring);
+            const uint32_t xdesc = umma_desc_lo(smem_u32(xsm)), ydesc = umma_desc_lo(smem_u32(ring));
+            Ring st(p.stages), bf(p.bufs);
             bool ok = true;
-            struct Walk {
-                int64_t w;
-                uint32_t n;
-                int seg;
-                int64_t unit_end;
-                bool first, last;
-                K6Unit u;
-            };
-            auto enter = [&](Walk& k) {  // at the first tile of a segment
-                k.u = line.unit(line.unit_of(k.w));
-                k.unit_end = k.u.begin + k.u.cols < w1 ? k.u.begin + k.u.cols : w1;
-                k.first = true;
-            };
-            Walk s, g;
-            s.w = g.w = w0;
-            s.n = g.n = 0;
-            s.seg = g.seg = 0;
-            auto issue_logits = [&]() -> bool {
-                if (s.n == 0 || s.w == s.unit_end) {
-                    if (s.n != 0) ++s.seg;
-                    enter(s);
-                    if (!mbar_wait(&ctl->xfull, s.seg & 1, abort)) return false;
-                }
-                const int st = s.n % p.stages, bf = s.n % p.bufs;
-                if (!mbar_wait(&ctl->pdone[bf], ((s.n / p.bufs) & 1) ^ 1, abort)) return false;
-                if (!mbar_wait(&ctl->full[st], (s.n / p.stages) & 1, abort)) return false;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc_cols + (uint32_t)(bf * TN);
-                for (int kc = 0; kc < p.kchunks; ++kc) {
-                    const uint32_t a = xbase + (uint32_t)(kc * XCHUNK);
-                    const uint32_t b = rbase + (uint32_t)(st * ystage + kc * YCHUNK);
+            int seg = 0;
+            for (int64_t w = w0; ok && w < w1; ++seg) {
+                const K6Unit u = line.unit(line.unit_of(w));
+                const int64_t end = u.begin + u.cols < w1 ? u.begin + u.cols : w1;
+                if (!mbar_wait(&ctl->xfull, seg & 1, abort)) { ok = false; break; }
+                for (; w < end; ++w) {
+                    if (!mbar_wait(&ctl->pdone[bf.at], bf.phase ^ 1, abort)) { ok = false; break; }
+                    if (!mbar_wait(&ctl->full[st.at], st.phase, abort)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + acc_cols + (uint32_t)(bf.at * TN);
+                    uint32_t a = xdesc, b = ydesc + (uint32_t)(st.at * ystage >> 4);
+                    for (int kc = 0; kc < p.kchunks; ++kc, a += XCHUNK >> 4, b += YCHUNK >> 4) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(d_tmem, umma_desc_kmajor_sw128(a + kk * 32), umma_desc_kmajor_sw128(b + kk * 32),
-                                  p.idesc_s, (kc | kk) != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_bf16(d_tmem, umma_desc_of(a + kk * 2, UMMA_KMAJOR_HI), umma_desc_of(b + kk * 2, UMMA_KMAJOR_HI),
+                                      p.idesc_s, (kc | kk) != 0 ? 1u : 0u);
+                    }
+                    umma_commit(&ctl->sfull[bf.at]);
+                    st.next();
+                    bf.next();
                 }
-                umma_commit(&ctl->sfull[bf]);
-                ++s.n;
-                ++s.w;
-                if (s.w == s.unit_end) umma_commit(&ctl->xempty);  // the kept tile is free after this
-                return true;
-            };
-            for (int q = 0; ok && q < p.ahead && s.w < w1; ++q) ok = issue_logits();
-            while (ok && g.w < w1) {
-                if (g.n == 0 || g.w == g.unit_end) {
-                    if (g.n != 0) ++g.seg;
-                    enter(g);
-                    if (!mbar_wait(&ctl->accempty, (g.seg & 1) ^ 1, abort)) { ok = false; break; }
-                }
-                const int st = g.n % p.stages, bf = g.n % p.bufs;
-                if (!mbar_wait(&ctl->pfull[bf], (g.n / p.bufs) & 1, abort)) { ok = false; break; }
-                tc_fence_after();
-                const int cols = p.d - g.u.half * K6_HALF < K6_HALF ? p.d - g.u.half * K6_HALF : K6_HALF;
-                const uint32_t idesc = umma_idesc_bf16_bmn(K6_M, cols);
-                const uint32_t a = tmem_base + acc_cols + (uint32_t)(bf * TN);
-                const uint32_t b = rbase + (uint32_t)(st * ystage + g.u.half * (K6_HALF / 64) * YCHUNK);
-#pragma unroll
-                for (int kk = 0; kk < TN / 16; ++kk)
-                    umma_bf16_ts(tmem_base, a + kk * 8, umma_desc_mnmajor_sw128(b + kk * 2048, YCHUNK), idesc,
-                                 g.first && kk == 0 ? 0u : 1u);
-                g.first = false;
-                umma_commit(&ctl->empty[st]);
-                umma_commit(&ctl->pdone[bf]);
-                ++g.n;
-                ++g.w;
-                if (g.w == g.unit_end) umma_commit(&ctl->accfull);
-                if (s.w < w1) ok = issue_logits();
+                if (ok) umma_commit(&ctl->xempty);  // the kept tile is free after this
             }
             if (!ok) {
                 atomicExch(p.err, ERR_TIMEOUT_MMA);
                 *abort = 1;
             }
             // Wait for every MMA issued by this thread before TMEM is freed.
-            umma_commit(&ctl->drain);
-            mbar_wait(&ctl->drain, 0, nullptr);
+            umma_commit(&ctl->drain[0]);
+            mbar_wait(&ctl->drain[0], 0, nullptr);
+        }
+    } else if (warp == 2 + K6_EPI_WARPS) {
+        // ------------------------------ products ------------------------------
+        // Another thread issues the product of every tile once P is there, and
+        // with it frees the tile's stage and buffer.
+        if (lane == 0) {
+            const uint32_t ydesc = umma_desc_lo(smem_u32(ring)) | ((uint32_t)(YCHUNK >> 4) << 16);
+            Ring st(p.stages), bf(p.bufs);
+            bool ok = true;
+            int seg = 0;
+            for (int64_t w = w0; ok && w < w1; ++seg) {
+                const K6Unit u = line.unit(line.unit_of(w));
+                const int64_t end = u.begin + u.cols < w1 ? u.begin + u.cols : w1;
+                const int cols = p.d - u.half * K6_HALF < K6_HALF ? p.d - u.half * K6_HALF : K6_HALF;
+                const uint32_t idesc = umma_idesc_bf16_bmn(K6_M, cols);
+                const uint32_t half = (uint32_t)(u.half * (K6_HALF / 64) * YCHUNK) >> 4;
+                uint32_t accumulate = 0;
+                if (!mbar_wait(&ctl->accempty, (seg & 1) ^ 1, abort)) { ok = false; break; }
+                for (; w < end; ++w) {
+                    if (!mbar_wait(&ctl->pfull[bf.at], bf.phase, abort)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a = tmem_base + acc_cols + (uint32_t)(bf.at * TN);
+                    const uint32_t b = ydesc + (uint32_t)(st.at * ystage >> 4) + half;
+#pragma unroll
+                    for (int kk = 0; kk < TN / 16; ++kk) {
+                        umma_bf16_ts(tmem_base, a + kk * 8, umma_desc_of(b + kk * (2048 >> 4), UMMA_MNMAJOR_HI), idesc,
+                                     accumulate);
+                        accumulate = 1;
+                    }
+                    umma_commit(&ctl->pdone[bf.at]);
+                    umma_commit(&ctl->empty[st.at]);
+                    st.next();
+                    bf.next();
+                }
+                if (ok) umma_commit(&ctl->accfull);
+            }
+            if (!ok) {
+                atomicExch(p.err, ERR_TIMEOUT_MMA);
+                *abort = 1;
+            }
+            umma_commit(&ctl->drain[1]);
+            mbar_wait(&ctl->drain[1], 0, nullptr);
         }
     } else {
         // ------------------------------ epilogue ------------------------------
@@ -417,6 +434,63 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
                 }
             };
             if (t < t1) load_cols(t);
+            // One chunk of 32 logits to 16 registers of P.
+            auto chunk = [&](Cols32& v, int tt, int c, uint32_t(&pk)[16], auto pass) {
+                const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
+                const int4* g4 = reinterpret_cast<const int4*>(grp_s + c * 32);
+                const float4* w4 = reinterpret_cast<const float4*>(wgt_s + c * 32);
+#pragma unroll
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    const float4 bb = b4[e4];
+                    float2 lo = fma2(make_float2(v.x[4 * e4], v.x[4 * e4 + 1]), a2v, make_float2(bb.x, bb.y));
+                    float2 hi = fma2(make_float2(v.x[4 * e4 + 2], v.x[4 * e4 + 3]), a2v, make_float2(bb.z, bb.w));
+                    lo = add2(lo, rowv);
+                    hi = add2(hi, rowv);
+                    if constexpr (HITS) {  // the diagonal among them
+                        const int4 gg = g4[e4];
+                        lo.x = gg.x == mine.grp ? -INFINITY : lo.x;
+                        lo.y = gg.y == mine.grp ? -INFINITY : lo.y;
+                        hi.x = gg.z == mine.grp ? -INFINITY : hi.x;
+                        hi.y = gg.w == mine.grp ? -INFINITY : hi.y;
+                    }
+                    v.x[4 * e4] = lo.x;
+                    v.x[4 * e4 + 1] = lo.y;
+                    v.x[4 * e4 + 2] = hi.x;
+                    v.x[4 * e4 + 3] = hi.y;
+                }
+                if constexpr (!HITS) {
+                    const int at = i - (tt * TN + c * 32);
+                    if ((unsigned)at < 32u) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v.x[e] = e == at ? -INFINITY : v.x[e];
+                    }
+                }
+#pragma unroll
+                for (int e4 = 0; e4 < 8; ++e4) {
+                    float2 lo = make_float2(ex2_approx(v.x[4 * e4]), ex2_approx(v.x[4 * e4 + 1]));
+                    float2 hi = make_float2(ex2_approx(v.x[4 * e4 + 2]), ex2_approx(v.x[4 * e4 + 3]));
+                    if constexpr (decltype(pass)::value == 1) {
+                        const float4 ww = w4[e4];
+                        lo = mul2(lo, make_float2(ww.x, ww.y));
+                        hi = mul2(hi, make_float2(ww.z, ww.w));
+                    }
+                    pk[2 * e4] = bf16x2_bits(lo.x, lo.y);
+                    pk[2 * e4 + 1] = bf16x2_bits(hi.x, hi.y);
+                }
+            };
+            // P of chunk c covers logits that this thread has read already.
+            auto tile = [&](uint32_t buf, int tt, auto pass) {
+#pragma unroll 1
+                for (int c = 0; c < TN / 32; ++c) {
+                    Cols32 v;
+                    uint32_t pk[16];
+                    tmem_ld_32cols(buf + c * 32, v.x);
+                    tmem_ld_wait();
+                    fence_regs(v);
+                    chunk(v, tt, c, pk, pass);
+                    tmem_st_16cols(buf + c * 16, pk);
+                }
+            };
             for (; t < t1; t += K6_GROUPS) {
                 const uint32_t nt = n + (uint32_t)(t - t0);
                 const int bf = nt % p.bufs;
@@ -432,57 +506,7 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
                 if (!mbar_wait(&ctl->sfull[bf], (nt / p.bufs) & 1, abort)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t buf = lane_base + acc_cols + (uint32_t)(bf * TN);
-#pragma unroll 1
-                for (int c = 0; c < TN / 32; ++c) {
-                    Cols32 v;
-                    tmem_ld_32cols(buf + c * 32, v.x);
-                    tmem_ld_wait();
-                    fence_regs(v);
-                    const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
-                    const int4* g4 = reinterpret_cast<const int4*>(grp_s + c * 32);
-                    const float4* w4 = reinterpret_cast<const float4*>(wgt_s + c * 32);
-#pragma unroll
-                    for (int e4 = 0; e4 < 8; ++e4) {
-                        const float4 bb = b4[e4];
-                        float2 lo = fma2(make_float2(v.x[4 * e4], v.x[4 * e4 + 1]), a2v, make_float2(bb.x, bb.y));
-                        float2 hi = fma2(make_float2(v.x[4 * e4 + 2], v.x[4 * e4 + 3]), a2v, make_float2(bb.z, bb.w));
-                        lo = add2(lo, rowv);
-                        hi = add2(hi, rowv);
-                        if constexpr (HITS) {  // the diagonal among them
-                            const int4 gg = g4[e4];
-                            lo.x = gg.x == mine.grp ? -INFINITY : lo.x;
-                            lo.y = gg.y == mine.grp ? -INFINITY : lo.y;
-                            hi.x = gg.z == mine.grp ? -INFINITY : hi.x;
-                            hi.y = gg.w == mine.grp ? -INFINITY : hi.y;
-                        }
-                        v.x[4 * e4] = lo.x;
-                        v.x[4 * e4 + 1] = lo.y;
-                        v.x[4 * e4 + 2] = hi.x;
-                        v.x[4 * e4 + 3] = hi.y;
-                    }
-                    if constexpr (!HITS) {
-                        const int at = i - (t * TN + c * 32);
-                        if ((unsigned)at < 32u) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v.x[e] = e == at ? -INFINITY : v.x[e];
-                        }
-                    }
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e4 = 0; e4 < 8; ++e4) {
-                        float2 lo = make_float2(ex2_approx(v.x[4 * e4]), ex2_approx(v.x[4 * e4 + 1]));
-                        float2 hi = make_float2(ex2_approx(v.x[4 * e4 + 2]), ex2_approx(v.x[4 * e4 + 3]));
-                        if (u.pass == 1) {
-                            const float4 ww = w4[e4];
-                            lo = mul2(lo, make_float2(ww.x, ww.y));
-                            hi = mul2(hi, make_float2(ww.z, ww.w));
-                        }
-                        pk[2 * e4] = bf16x2_bits(lo.x, lo.y);
-                        pk[2 * e4 + 1] = bf16x2_bits(hi.x, hi.y);
-                    }
-                    // P of chunk c covers logits that this thread has read already
-                    tmem_st_16cols(buf + c * 16, pk);
-                }
+                if (u.pass == 0) tile(buf, t, Pass<0>{}); else tile(buf, t, Pass<1>{});
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -622,7 +646,6 @@ SoftmaxGradPlan softmax_grad_plan(int b, int nc, int d, bool item_ids, bool copi
     pl.bufs = (K6_TMEM_COLS - acc) / pl.tile_cols;
     if (pl.bufs > K6_MAX_BUFS) pl.bufs = K6_MAX_BUFS;
     pl.stages = pl.tile_cols == 128 ? stages_for<128>(kchunks) : stages_for<64>(kchunks);
-    pl.ahead = pl.bufs - 1 < pl.stages ? pl.bufs - 1 : pl.stages;
     int64_t units;
     if (pl.tile_cols == 128) {
         const K6Line<128> line(b, nc);
@@ -724,7 +747,6 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     p.width = pl.width;
     p.stages = pl.stages;
     p.bufs = pl.bufs;
-    p.ahead = pl.ahead;
     p.work = pl.work;
     p.idesc_s = umma_idesc_bf16(K6_M, TN);
     e = hits ? launch_products<TN, true>(pl, g, p, s) : launch_products<TN, false>(pl, g, p, s);

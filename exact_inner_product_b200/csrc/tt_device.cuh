@@ -293,16 +293,22 @@ __device__ __forceinline__ uint64_t umma_desc_kmajor_sw128(uint32_t start) {
 }
 
 // The same TMA box read as an MN-major operand: its rows run along K, its 64
-// elements per row along N. Blocks of 64 elements of N lie `block_bytes` apart
-// (one box each), groups of 8 rows of K 1024 bytes; K steps of 16 advance
-// start by 2048.
-__device__ __forceinline__ uint64_t umma_desc_mnmajor_sw128(uint32_t start, uint32_t block_bytes) {
-    uint64_t desc = 0;
-    desc |= (uint64_t)((start >> 4) & 0x3FFFu);              // start address, bits 0-13
-    desc |= (uint64_t)((block_bytes >> 4) & 0x3FFFu) << 16;  // leading byte offset: next 64 elements of N
-    desc |= (uint64_t)(1024u >> 4) << 32;                    // stride byte offset: next 8 rows of K
-    desc |= (uint64_t)1u << 46;                              // descriptor version (sm_100)
-    desc |= (uint64_t)2u << 61;                              // layout: 128-byte swizzle
+// elements per row along N. Blocks of 64 elements of N lie a leading byte
+// offset apart (one box each), groups of 8 rows of K 1024 bytes; K steps of 16
+// advance start by 2048.
+//
+// Descriptors in two halves, for loops that only move the start: the upper
+// half is constant (stride 1024 bytes, version, 128-byte swizzle, the same for
+// both), the lower half holds start >> 4 and, from bit 16, the leading byte
+// offset >> 4 (K-major: not used).
+constexpr uint32_t UMMA_KMAJOR_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t UMMA_MNMAJOR_HI = UMMA_KMAJOR_HI;
+
+__device__ __forceinline__ uint32_t umma_desc_lo(uint32_t start) { return (start >> 4) & 0x3FFFu; }
+
+__device__ __forceinline__ uint64_t umma_desc_of(uint32_t lo, uint32_t hi) {
+    uint64_t desc;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(desc) : "r"(lo), "r"(hi));
     return desc;
 }
 

@@ -308,7 +308,7 @@ cudaError_t launch_embedding_grad(const EmbeddingGrad& g, bool by_row, cudaStrea
 // The gradient of the in-batch softmax (k_softmax_grad.cu): work split and
 // workspace layout (the error word is at offset 0).
 struct SoftmaxGradPlan {
-    int tile_cols, halves, width, bufs, stages, ahead, grid, log2_slots;
+    int tile_cols, halves, width, bufs, stages, grid, log2_slots;
     int64_t work;
     size_t off_err, off_item, off_user, off_weight, off_diag, off_keys, off_users_c, off_items_c, off_part;
     size_t bytes;

@@ -75,7 +75,9 @@ __device__ __forceinline__ int item_group(unsigned long long id, unsigned long l
     // so a free or matching slot is always found
     int64_t h = table_hash(id, log2_slots);
     for (int64_t probe = 0; probe < slots; ++probe) {
-        const unsigned long long prev = atomicCAS(keys + h, TABLE_EMPTY, id);
+        // a popular id is found by a plain read, without the atomic's queue
+        unsigned long long prev = *reinterpret_cast<volatile unsigned long long*>(keys + h);
+        if (prev == TABLE_EMPTY) prev = atomicCAS(keys + h, TABLE_EMPTY, id);
         if (prev == TABLE_EMPTY || prev == id) return (int)h;
         h = (h + 1) & (slots - 1);
     }
