@@ -56,7 +56,10 @@ namespace tt {
 namespace {
 
 constexpr int K6_M = 128;            // kept rows per tile (TMEM lanes)
-constexpr int K6_GROUPS = 3;         // groups of four epilogue warps, one tile each in turn
+#ifndef VG
+#define VG 2
+#endif
+constexpr int K6_GROUPS = VG;         // groups of four epilogue warps, one tile each in turn
 constexpr int K6_EPI_WARPS = 4 * K6_GROUPS;
 constexpr int K6_THREADS = 32 * (3 + K6_EPI_WARPS);
 constexpr int K6_TMEM_COLS = 512;
@@ -67,7 +70,6 @@ constexpr int K6_HALF = 256;         // widest product of one unit; wider rows t
 constexpr float K6_LOG2E = 1.4426950408889634f;
 constexpr int K6_PREP_THREADS = 256;
 
-template <int TN>
 struct K6Ctl {
     uint64_t full[K6_MAX_STAGES], empty[K6_MAX_STAGES];
     uint64_t xfull, xempty;
@@ -78,13 +80,9 @@ struct K6Ctl {
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
-    // per epilogue warp: bias, group and weight of its tile's columns
-    alignas(16) float bias[K6_EPI_WARPS][TN];
-    alignas(16) int grp[K6_EPI_WARPS][TN];
-    alignas(16) float wgt[K6_EPI_WARPS][TN];
 };
 
-struct K6Side {
+struct alignas(8) K6Side {
     float bias;  // added to acc log2(e) / tau: items -log q log2(e); users -lse log2(e), -inf where w = 0
     int grp;     // item group
 };
@@ -100,6 +98,7 @@ struct K6Params {
     int kchunks;          // 64-element pieces of a row
     int halves, width;    // products of `width` columns, in `halves` units
     int stages, bufs;
+    int weighted;         // the items' pass multiplies P by w_i (else the rows' common weight is applied at the end)
     int64_t work;         // tiles in all
     uint32_t idesc_s;
 };
@@ -152,7 +151,7 @@ struct K6Prep {
     unsigned long long* keys;
     int log2_slots;
     K6Side *item, *user;
-    float *weight, *diag;
+    float *weight, *diag, *common;
     const uint4 *users, *items;  // copied where valid is given
     uint4 *users_c, *items_c;
     int b, nc, vpr;              // vpr: 16-byte pieces of a row
@@ -173,7 +172,10 @@ __global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
         if ((threadIdx.x & 31) == 0) atomicAdd(&valid_rows, n);
         __syncthreads();
     }
-    const float mean_w = p.grad_mean != nullptr ? *p.grad_mean / (float)(p.valid != nullptr ? valid_rows : p.b) : 0.f;
+    // the weight of every valid row, where there is no gradient per row
+    const int count = p.valid != nullptr ? valid_rows : p.b;
+    const float mean_w = p.grad_mean != nullptr && count > 0 ? *p.grad_mean / (float)count : 0.f;
+    if (tid == 0) *p.common = p.grad_loss != nullptr ? 1.f : mean_w;
     for (int j = tid; j < p.nc; j += threads) {
         const bool ok = p.valid == nullptr || p.valid[j] != 0;
         K6Side c;
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
     uint8_t* xsm = smem;                                   // [kchunks][128 x 128 B]
     uint8_t* ring = smem + (size_t)p.kchunks * XCHUNK;     // [stages][kchunks][TN x 128 B]
     const int ystage = p.kchunks * YCHUNK;
-    K6Ctl<TN>* ctl = reinterpret_cast<K6Ctl<TN>*>(ring + (size_t)p.stages * ystage);
+    K6Ctl* ctl = reinterpret_cast<K6Ctl*>(ring + (size_t)p.stages * ystage);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -397,15 +399,16 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
     } else {
         // ------------------------------ epilogue ------------------------------
         // Group g takes tiles g, g + K6_GROUPS, ...; warp w of it TMEM lanes
-        // 32 (w % 4) .., one kept row per thread, all TN columns of the tile.
+        // 32 (w % 4) .., as two blocks of 16 in the fragment layout: a thread has
+        // rows lane / 4 + {0, 8, 16, 24} and, of each 8 columns, the pair
+        // 2 (lane % 4). Its columns' constants then fit in registers (a whole row
+        // per thread would read them all from shared memory, at the cost of the
+        // exponentials themselves).
         const int ew = warp - 2;
         const int group = ew >> 2;
         const int quarter = warp & 3;
         const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
         const float2 a2v = make_float2(p.a2, p.a2);
-        float* bias_s = ctl->bias[ew];
-        int* grp_s = ctl->grp[ew];
-        float* wgt_s = ctl->wgt[ew];
         bool ok = true;
         uint32_t n = 0;
         int seg = 0;
@@ -417,96 +420,88 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
             const int rows = u.pass == 0 ? p.b : p.nc, cols = u.pass == 0 ? p.nc : p.b;
             const K6Side* xs = u.pass == 0 ? p.user : p.item;
             const K6Side* ys = u.pass == 0 ? p.item : p.user;
-            const int i = u.tile * K6_M + quarter * 32 + lane;
-            K6Side mine = {-INFINITY, -1};
-            if (i < rows) mine = xs[i];
-            const float2 rowv = make_float2(mine.bias, mine.bias);
-            // first tile of this segment that is this group's
-            int t = t0 + (int)((K6_GROUPS + group - n % K6_GROUPS) % K6_GROUPS);
-            int2 cv[TN / 32];
-            float cw[TN / 32];
-            auto load_cols = [&](int tt) {
+            const int row0 = u.tile * K6_M + quarter * 32 + (lane >> 2);
+            const int col0 = 2 * (lane & 3);
+            float rbias[4];
+            int rgrp[4];
 #pragma unroll
-                for (int e = 0; e < TN / 32; ++e) {
-                    const int j = tt * TN + 32 * e + lane;
-                    cv[e] = j < cols ? __ldg(reinterpret_cast<const int2*>(ys) + j) : make_int2((int)0xff800000u, -2);
-                    cw[e] = u.pass == 1 && j < cols ? __ldg(p.weight + j) : 0.f;
+            for (int q = 0; q < 4; ++q) {
+                const bool in = row0 + 8 * q < rows;
+                rbias[q] = in ? xs[row0 + 8 * q].bias : -INFINITY;
+                rgrp[q] = in ? xs[row0 + 8 * q].grp : -1;
+            }
+            // the constants of this thread's columns of tile tt
+            auto columns = [&](int4 (&cc)[TN / 8], int tt) {
+#pragma unroll
+                for (int e = 0; e < TN / 8; ++e) {
+                    const int j = tt * TN + 8 * e + col0;
+                    cc[e] = make_int4((int)0xff800000u, -2, (int)0xff800000u, -2);
+                    if (j + 1 < cols) cc[e] = __ldg(reinterpret_cast<const int4*>(ys + j));
+                    else if (j < cols) cc[e].x = __float_as_int(ys[j].bias), cc[e].y = ys[j].grp;
                 }
             };
-            if (t < t1) load_cols(t);
-            // One chunk of 32 logits to 16 registers of P.
-            auto chunk = [&](Cols32& v, int tt, int c, uint32_t(&pk)[16], auto pass) {
-                const float4* b4 = reinterpret_cast<const float4*>(bias_s + c * 32);
-                const int4* g4 = reinterpret_cast<const int4*>(grp_s + c * 32);
-                const float4* w4 = reinterpret_cast<const float4*>(wgt_s + c * 32);
-#pragma unroll
-                for (int e4 = 0; e4 < 8; ++e4) {
-                    const float4 bb = b4[e4];
-                    float2 lo = fma2(make_float2(v.x[4 * e4], v.x[4 * e4 + 1]), a2v, make_float2(bb.x, bb.y));
-                    float2 hi = fma2(make_float2(v.x[4 * e4 + 2], v.x[4 * e4 + 3]), a2v, make_float2(bb.z, bb.w));
-                    lo = add2(lo, rowv);
-                    hi = add2(hi, rowv);
-                    if constexpr (HITS) {  // the diagonal among them
-                        const int4 gg = g4[e4];
-                        lo.x = gg.x == mine.grp ? -INFINITY : lo.x;
-                        lo.y = gg.y == mine.grp ? -INFINITY : lo.y;
-                        hi.x = gg.z == mine.grp ? -INFINITY : hi.x;
-                        hi.y = gg.w == mine.grp ? -INFINITY : hi.y;
-                    }
-                    v.x[4 * e4] = lo.x;
-                    v.x[4 * e4 + 1] = lo.y;
-                    v.x[4 * e4 + 2] = hi.x;
-                    v.x[4 * e4 + 3] = hi.y;
-                }
+            // 64 columns of one 16-row block to P, which covers logits that the
+            // block's threads have read already.
+            auto step = [&](uint32_t buf, const int4 (&cc)[TN / 8], int tt, int h, int k, auto pass) {
+                float v[32];
+                uint32_t pk[16];
+                const uint32_t at = buf + ((uint32_t)(16 * k) << 16);
+                tmem_ld_frag64(at + h * 64, v);
+                tmem_ld_wait();
+                fence_regs(v);
+                bool diagonal = false;  // (without item ids) a column equal to a row in this step
                 if constexpr (!HITS) {
-                    const int at = i - (tt * TN + c * 32);
-                    if ((unsigned)at < 32u) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v.x[e] = e == at ? -INFINITY : v.x[e];
-                    }
+                    const int r0 = u.tile * K6_M + quarter * 32 + 16 * k, c0 = tt * TN + h * 64;
+                    diagonal = r0 < c0 + 64 && c0 < r0 + 16;
                 }
 #pragma unroll
-                for (int e4 = 0; e4 < 8; ++e4) {
-                    float2 lo = make_float2(ex2_approx(v.x[4 * e4]), ex2_approx(v.x[4 * e4 + 1]));
-                    float2 hi = make_float2(ex2_approx(v.x[4 * e4 + 2]), ex2_approx(v.x[4 * e4 + 3]));
-                    if constexpr (decltype(pass)::value == 1) {
-                        const float4 ww = w4[e4];
-                        lo = mul2(lo, make_float2(ww.x, ww.y));
-                        hi = mul2(hi, make_float2(ww.z, ww.w));
+                for (int e = 0; e < 8; ++e) {
+                    const int4 c = cc[8 * h + e];
+                    const float2 bb = make_float2(__int_as_float(c.x), __int_as_float(c.z));
+                    float2 ww = make_float2(1.f, 1.f);
+                    if constexpr (decltype(pass)::value == 2) {
+                        const int j = tt * TN + h * 64 + 8 * e + col0;
+                        ww.x = j < cols ? __ldg(p.weight + j) : 0.f;
+                        ww.y = j + 1 < cols ? __ldg(p.weight + j + 1) : 0.f;
                     }
-                    pk[2 * e4] = bf16x2_bits(lo.x, lo.y);
-                    pk[2 * e4 + 1] = bf16x2_bits(hi.x, hi.y);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float rb = rbias[2 * k + q];
+                        float2 x = fma2(make_float2(v[4 * e + 2 * q], v[4 * e + 2 * q + 1]), a2v, bb);
+                        x = add2(x, make_float2(rb, rb));
+                        if constexpr (HITS) {  // the diagonal among them
+                            x.x = c.y == rgrp[2 * k + q] ? -INFINITY : x.x;
+                            x.y = c.w == rgrp[2 * k + q] ? -INFINITY : x.y;
+                        } else if (diagonal) {
+                            const int i = row0 + 16 * k + 8 * q, j = tt * TN + h * 64 + 8 * e + col0;
+                            x.x = i == j ? -INFINITY : x.x;
+                            x.y = i == j + 1 ? -INFINITY : x.y;
+                        }
+                        float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        if constexpr (decltype(pass)::value == 2) y = mul2(y, ww);
+                        pk[2 * e + q] = bf16x2_bits(y.x, y.y);
+                    }
+                }
+                tmem_st_frag32(at + h * 32, pk);
+            };
+            auto tile = [&](uint32_t buf, const int4 (&cc)[TN / 8], int tt, auto pass) {
+#pragma unroll
+                for (int h = 0; h < TN / 64; ++h) {
+                    step(buf, cc, tt, h, 0, pass);
+                    step(buf, cc, tt, h, 1, pass);
                 }
             };
-            // P of chunk c covers logits that this thread has read already.
-            auto tile = [&](uint32_t buf, int tt, auto pass) {
-#pragma unroll 1
-                for (int c = 0; c < TN / 32; ++c) {
-                    Cols32 v;
-                    uint32_t pk[16];
-                    tmem_ld_32cols(buf + c * 32, v.x);
-                    tmem_ld_wait();
-                    fence_regs(v);
-                    chunk(v, tt, c, pk, pass);
-                    tmem_st_16cols(buf + c * 16, pk);
-                }
-            };
-            for (; t < t1; t += K6_GROUPS) {
+            const int kind = u.pass == 0 || !p.weighted ? 1 : 2;
+            // first tile of this segment that is this group's
+            for (int t = t0 + (int)((K6_GROUPS + group - n % K6_GROUPS) % K6_GROUPS); t < t1; t += K6_GROUPS) {
                 const uint32_t nt = n + (uint32_t)(t - t0);
                 const int bf = nt % p.bufs;
-                __syncwarp();  // the previous tile's reads are done
-#pragma unroll
-                for (int e = 0; e < TN / 32; ++e) {
-                    bias_s[32 * e + lane] = __int_as_float(cv[e].x);
-                    if (HITS) grp_s[32 * e + lane] = cv[e].y;
-                    if (u.pass == 1) wgt_s[32 * e + lane] = cw[e];
-                }
-                __syncwarp();
-                if (t + K6_GROUPS < t1) load_cols(t + K6_GROUPS);
+                int4 cc[TN / 8];
+                columns(cc, t);
                 if (!mbar_wait(&ctl->sfull[bf], (nt / p.bufs) & 1, abort)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t buf = lane_base + acc_cols + (uint32_t)(bf * TN);
-                if (u.pass == 0) tile(buf, t, Pass<0>{}); else tile(buf, t, Pass<1>{});
+                if (kind == 1) tile(buf, cc, t, Pass<1>{}); else tile(buf, cc, t, Pass<2>{});
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -554,6 +549,7 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
 struct K6Finish {
     const float* part;
     const float *weight, *diag;  // [b]
+    const float* common;         // factor of the items' products
     const __nv_bfloat16 *users, *items;
     __nv_bfloat16 *grad_users, *grad_items;
     const int* err;
@@ -569,6 +565,7 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
     const int vpr = p.d / 8;
     const int64_t total = ((int64_t)p.b + p.nc) * vpr;
     const bool failed = *p.err != 0;
+    const float common = *p.common;
     for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < total; v += (int64_t)gridDim.x * 256) {
         const int64_t r = v / vpr;
         const int col = (int)(v - r * vpr) * 8;
@@ -590,6 +587,10 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
             const float4 x = __ldg(q), y = __ldg(q + 1);
             acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
             acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
+        }
+        if (pass == 1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] *= common;
         }
         const float w = i < p.b ? p.weight[i] : 0.f;
         float out[8];
@@ -626,7 +627,7 @@ int log2_ceil(int64_t x) {
 
 template <int TN>
 int stages_for(int kchunks) {
-    const int fixed = 1024 + kchunks * K6_M * 128 + (int)sizeof(K6Ctl<TN>);
+    const int fixed = 1024 + kchunks * K6_M * 128 + (int)sizeof(K6Ctl);
     const int s = (K6_SMEM_BUDGET - fixed) / (kchunks * TN * 128);
     return s < K6_MAX_STAGES ? s : K6_MAX_STAGES;
 }
@@ -669,6 +670,7 @@ SoftmaxGradPlan softmax_grad_plan(int b, int nc, int d, bool item_ids, bool copi
     pl.off_user = take((size_t)b * sizeof(K6Side));
     pl.off_weight = take((size_t)b * sizeof(float));
     pl.off_diag = take((size_t)b * sizeof(float));
+    pl.off_common = take(sizeof(float));
     pl.off_keys = take(item_ids ? ((size_t)1 << pl.log2_slots) * sizeof(unsigned long long) : 0);
     pl.off_users_c = take(copies ? (size_t)b * d * 2 : 0);
     pl.off_items_c = take(copies ? (size_t)nc * d * 2 : 0);
@@ -681,7 +683,7 @@ namespace {
 
 template <int TN, bool HITS>
 cudaError_t launch_products(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, const K6Params& p, cudaStream_t s) {
-    const int smem = 1024 + p.kchunks * K6_M * 128 + p.stages * p.kchunks * TN * 128 + (int)sizeof(K6Ctl<TN>);
+    const int smem = 1024 + p.kchunks * K6_M * 128 + p.stages * p.kchunks * TN * 128 + (int)sizeof(K6Ctl);
     cudaError_t e = cudaFuncSetAttribute(k6_products<TN, HITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
@@ -718,6 +720,7 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     q.user = reinterpret_cast<K6Side*>(ws + pl.off_user);
     q.weight = reinterpret_cast<float*>(ws + pl.off_weight);
     q.diag = reinterpret_cast<float*>(ws + pl.off_diag);
+    q.common = reinterpret_cast<float*>(ws + pl.off_common);
     q.users = static_cast<const uint4*>(g.users);
     q.items = static_cast<const uint4*>(g.items);
     q.users_c = reinterpret_cast<uint4*>(ws + pl.off_users_c);
@@ -747,6 +750,7 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     p.width = pl.width;
     p.stages = pl.stages;
     p.bufs = pl.bufs;
+    p.weighted = g.grad_loss != nullptr ? 1 : 0;
     p.work = pl.work;
     p.idesc_s = umma_idesc_bf16(K6_M, TN);
     e = hits ? launch_products<TN, true>(pl, g, p, s) : launch_products<TN, false>(pl, g, p, s);
@@ -756,6 +760,7 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     f.part = p.part;
     f.weight = q.weight;
     f.diag = q.diag;
+    f.common = q.common;
     const bool copies = g.valid != nullptr;
     f.users = static_cast<const __nv_bfloat16*>(copies ? static_cast<const void*>(q.users_c) : g.users);
     f.items = static_cast<const __nv_bfloat16*>(copies ? static_cast<const void*>(q.items_c) : g.items);

@@ -33,15 +33,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 // Keep the compiler from moving uses of TMEM-loaded registers above the
 // tcgen05.wait::ld that makes them valid.
-__device__ __forceinline__ void fence_regs(Cols32& c) {
+__device__ __forceinline__ void fence_regs(float (&x)[32]) {
     asm volatile(""
-                 : "+f"(c.x[0]), "+f"(c.x[1]), "+f"(c.x[2]), "+f"(c.x[3]), "+f"(c.x[4]), "+f"(c.x[5]),
-                   "+f"(c.x[6]), "+f"(c.x[7]), "+f"(c.x[8]), "+f"(c.x[9]), "+f"(c.x[10]), "+f"(c.x[11]),
-                   "+f"(c.x[12]), "+f"(c.x[13]), "+f"(c.x[14]), "+f"(c.x[15]), "+f"(c.x[16]), "+f"(c.x[17]),
-                   "+f"(c.x[18]), "+f"(c.x[19]), "+f"(c.x[20]), "+f"(c.x[21]), "+f"(c.x[22]), "+f"(c.x[23]),
-                   "+f"(c.x[24]), "+f"(c.x[25]), "+f"(c.x[26]), "+f"(c.x[27]), "+f"(c.x[28]), "+f"(c.x[29]),
-                   "+f"(c.x[30]), "+f"(c.x[31]));
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]),
+                   "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]),
+                   "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]), "+f"(x[16]), "+f"(x[17]),
+                   "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]),
+                   "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]),
+                   "+f"(x[30]), "+f"(x[31]));
 }
+__device__ __forceinline__ void fence_regs(Cols32& c) { fence_regs(c.x); }
 
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
