@@ -56,12 +56,17 @@ namespace tt {
 namespace {
 
 constexpr int K6_M = 128;            // kept rows per tile (TMEM lanes)
-#ifndef VG
-#define VG 2
-#endif
-constexpr int K6_GROUPS = VG;         // groups of four epilogue warps, one tile each in turn
+constexpr int K6_GROUPS = 2;         // groups of four epilogue warps, one tile each in turn
 constexpr int K6_EPI_WARPS = 4 * K6_GROUPS;
-constexpr int K6_THREADS = 32 * (3 + K6_EPI_WARPS);
+constexpr int K6_THREADS = 32 * (4 + K6_EPI_WARPS);  // warps 0-3: copies, logits, products, none
+// Registers: the four first warps give back what the epilogue takes.
+// setmaxnreg.inc draws on the registers the block was launched with, and a
+// split above them would wait forever: launch_products refuses it.
+constexpr int K6_ROLE_REGS = 64;
+constexpr int K6_EPI_REGS = 208;
+constexpr int K6_SPLIT_REGS = 128 * K6_ROLE_REGS + 32 * K6_EPI_WARPS * K6_EPI_REGS;
+static_assert(K6_THREADS % 128 == 0, "whole warpgroups: setmaxnreg is theirs");
+static_assert(K6_SPLIT_REGS <= 16384 / (K6_THREADS / 32 / 4 * 32) / 8 * 8 * K6_THREADS, "register split");
 constexpr int K6_TMEM_COLS = 512;
 constexpr int K6_MAX_BUFS = 4;       // logit tiles in tensor memory
 constexpr int K6_MAX_STAGES = 8;
@@ -81,16 +86,20 @@ struct K6Ctl {
     uint32_t tmem_base;
     int abort;
 };
+static_assert(sizeof(K6Ctl) <= 1024, "the control block's place in shared memory");
 
-struct alignas(8) K6Side {
-    float bias;  // added to acc log2(e) / tau: items -log q log2(e); users -lse log2(e), -inf where w = 0
-    int grp;     // item group
+// What a row brings as one of a tile's columns or kept rows (arrays padded to
+// whole tiles): bias, added to acc log2(e) / tau (items -log q log2(e), users
+// -lse log2(e), -inf where w = 0), and the item group.
+struct K6Side {
+    float* bias;
+    int* grp;
 };
 
 struct K6Params {
-    const K6Side* item;   // [nc]
-    const K6Side* user;   // [b]
-    const float* weight;  // [b] w_i
+    K6Side item;          // [nc]
+    K6Side user;          // [b]
+    const float* weight;  // [b] w_i, padded
     float* part;          // [units + grid][128][width] partial products
     int* err;
     int b, nc, d;
@@ -150,7 +159,7 @@ struct K6Prep {
     const float *lse, *loss, *grad_loss, *grad_mean;
     unsigned long long* keys;
     int log2_slots;
-    K6Side *item, *user;
+    K6Side item, user;
     float *weight, *diag, *common;
     const uint4 *users, *items;  // copied where valid is given
     uint4 *users_c, *items_c;
@@ -176,18 +185,27 @@ __global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
     const int count = p.valid != nullptr ? valid_rows : p.b;
     const float mean_w = p.grad_mean != nullptr && count > 0 ? *p.grad_mean / (float)count : 0.f;
     if (tid == 0) *p.common = p.grad_loss != nullptr ? 1.f : mean_w;
+    // past the end, to whole tiles: columns without a share
+    for (int j = p.nc + tid; j < (p.nc + K6_M - 1) / K6_M * K6_M; j += threads) {
+        p.item.bias[j] = -INFINITY;
+        p.item.grp[j] = -2;
+    }
+    for (int j = p.b + tid; j < (p.b + K6_M - 1) / K6_M * K6_M; j += threads) {
+        p.user.bias[j] = -INFINITY;
+        p.user.grp[j] = -2;
+        p.weight[j] = 0.f;
+    }
     for (int j = tid; j < p.nc; j += threads) {
         const bool ok = p.valid == nullptr || p.valid[j] != 0;
-        K6Side c;
-        c.bias = ok ? (p.logq != nullptr ? -p.logq[j] * K6_LOG2E : 0.f) : -INFINITY;
-        c.grp = p.item_ids != nullptr ? item_group((unsigned long long)p.item_ids[j], p.keys, p.log2_slots) : 0;
-        p.item[j] = c;
+        p.item.bias[j] = ok ? (p.logq != nullptr ? -p.logq[j] * K6_LOG2E : 0.f) : -INFINITY;
+        const int grp = p.item_ids != nullptr ? item_group((unsigned long long)p.item_ids[j], p.keys, p.log2_slots) : 0;
+        p.item.grp[j] = grp;
         if (j < p.b) {
             const float w = ok ? (p.grad_loss != nullptr ? p.grad_loss[j] : 0.f) + mean_w : 0.f;
             p.weight[j] = w;
             p.diag[j] = ok ? expm1f(-p.loss[j]) : 0.f;
-            c.bias = w != 0.f ? -p.lse[j] * K6_LOG2E : -INFINITY;
-            p.user[j] = c;
+            p.user.bias[j] = w != 0.f ? -p.lse[j] * K6_LOG2E : -INFINITY;
+            p.user.grp[j] = grp;
         }
     }
     if (p.valid == nullptr) return;
@@ -203,16 +221,6 @@ __global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
 // ---------------------------------------------------------------------------
 // the products
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
-        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // A place in a ring of buffers and the parity of its current round.
 struct Ring {
     int at, len;
@@ -226,9 +234,9 @@ struct Ring {
     }
 };
 
-template <int P>
-struct Pass {
-    static constexpr int value = P;
+template <int K>
+struct Kind {
+    static constexpr int value = K;
 };
 
 template <int TN, bool HITS>
@@ -243,7 +251,9 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
     uint8_t* xsm = smem;                                   // [kchunks][128 x 128 B]
     uint8_t* ring = smem + (size_t)p.kchunks * XCHUNK;     // [stages][kchunks][TN x 128 B]
     const int ystage = p.kchunks * YCHUNK;
-    K6Ctl* ctl = reinterpret_cast<K6Ctl*>(ring + (size_t)p.stages * ystage);
+    // [stages][3][TN]: bias, group, weight of the stage's rows
+    float* cols_sm = reinterpret_cast<float*>(ring + (size_t)p.stages * ystage);
+    K6Ctl* ctl = reinterpret_cast<K6Ctl*>(cols_sm + (size_t)p.stages * 3 * TN);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -281,6 +291,8 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
     const uint32_t acc_cols = (uint32_t)((p.width + 31) / 32 * 32);  // the product; the logit tiles follow
     volatile int* abort = &ctl->abort;
 
+    if (warp < 4) {
+    regs_dec<K6_ROLE_REGS>();
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         if (lane == 0) {
@@ -300,7 +312,13 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
                 for (int t = t0; t < t1; ++t, ++n) {
                     const int s = n % p.stages;
                     if (!mbar_wait(&ctl->empty[s], ((n / p.stages) & 1) ^ 1, abort)) { ok = false; break; }
-                    mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)ystage);
+                    const bool weights = u.pass == 1 && p.weighted;
+                    const K6Side& ys = u.pass == 0 ? p.item : p.user;
+                    float* cs = cols_sm + s * 3 * TN;
+                    mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)(ystage + (1 + HITS + weights) * TN * 4));
+                    bulk_load(cs, ys.bias + (int64_t)t * TN, &ctl->full[s], TN * 4);
+                    if (HITS) bulk_load(cs + TN, ys.grp + (int64_t)t * TN, &ctl->full[s], TN * 4);
+                    if (weights) bulk_load(cs + 2 * TN, p.weight + (int64_t)t * TN, &ctl->full[s], TN * 4);
                     for (int kc = 0; kc < p.kchunks; ++kc)
                         tma_load_2d(ring + (size_t)s * ystage + (size_t)kc * YCHUNK, ty, &ctl->full[s], kc * 64, t * TN);
                 }
@@ -354,7 +372,7 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
             umma_commit(&ctl->drain[0]);
             mbar_wait(&ctl->drain[0], 0, nullptr);
         }
-    } else if (warp == 2 + K6_EPI_WARPS) {
+    } else if (warp == 2) {
         // ------------------------------ products ------------------------------
         // Another thread issues the product of every tile once P is there, and
         // with it frees the tile's stage and buffer.
@@ -396,7 +414,9 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
             umma_commit(&ctl->drain[1]);
             mbar_wait(&ctl->drain[1], 0, nullptr);
         }
+    }
     } else {
+        regs_inc<K6_EPI_REGS>();
         // ------------------------------ epilogue ------------------------------
         // Group g takes tiles g, g + K6_GROUPS, ...; warp w of it TMEM lanes
         // 32 (w % 4) .., as two blocks of 16 in the fragment layout: a thread has
@@ -404,108 +424,120 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
         // 2 (lane % 4). Its columns' constants then fit in registers (a whole row
         // per thread would read them all from shared memory, at the cost of the
         // exponentials themselves).
-        const int ew = warp - 2;
-        const int group = ew >> 2;
+        const int ew = warp - 4;
+        const int group = ew / (4);
         const int quarter = warp & 3;
         const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16);
-        const float2 a2v = make_float2(p.a2, p.a2);
+        const f32x2 a2v = pair(p.a2, p.a2);
         bool ok = true;
-        uint32_t n = 0;
+        Ring st(p.stages), bf(p.bufs);
+        int turn = 0;  // the group of the tile that st and bf stand at
+        auto step_on = [&](int& t) {
+            ++t;
+            st.next();
+            bf.next();
+            turn = turn + 1 == K6_GROUPS ? 0 : turn + 1;
+        };
         int seg = 0;
         for (int64_t w = w0; ok && w < w1; ++seg) {
             const int uid = line.unit_of(w);
             const K6Unit u = line.unit(uid);
             const int t0 = (int)(w - u.begin);
             const int t1 = (int)(u.begin + u.cols < w1 ? u.cols : w1 - u.begin);
-            const int rows = u.pass == 0 ? p.b : p.nc, cols = u.pass == 0 ? p.nc : p.b;
-            const K6Side* xs = u.pass == 0 ? p.user : p.item;
-            const K6Side* ys = u.pass == 0 ? p.item : p.user;
+            const int rows = u.pass == 0 ? p.b : p.nc;
+            const K6Side& xs = u.pass == 0 ? p.user : p.item;
             const int row0 = u.tile * K6_M + quarter * 32 + (lane >> 2);
             const int col0 = 2 * (lane & 3);
-            float rbias[4];
+            f32x2 rbias[4];
             int rgrp[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const bool in = row0 + 8 * q < rows;
-                rbias[q] = in ? xs[row0 + 8 * q].bias : -INFINITY;
-                rgrp[q] = in ? xs[row0 + 8 * q].grp : -1;
+                const int row = row0 + 8 * q;
+                const bool in = row < rows;
+                const float rb = in ? xs.bias[row] : -INFINITY;
+                rbias[q] = pair(rb, rb);
+                rgrp[q] = in ? xs.grp[row] : -1;
             }
-            // the constants of this thread's columns of tile tt
-            auto columns = [&](int4 (&cc)[TN / 8], int tt) {
-#pragma unroll
-                for (int e = 0; e < TN / 8; ++e) {
-                    const int j = tt * TN + 8 * e + col0;
-                    cc[e] = make_int4((int)0xff800000u, -2, (int)0xff800000u, -2);
-                    if (j + 1 < cols) cc[e] = __ldg(reinterpret_cast<const int4*>(ys + j));
-                    else if (j < cols) cc[e].x = __float_as_int(ys[j].bias), cc[e].y = ys[j].grp;
-                }
-            };
-            // 64 columns of one 16-row block to P, which covers logits that the
-            // block's threads have read already.
-            auto step = [&](uint32_t buf, const int4 (&cc)[TN / 8], int tt, int h, int k, auto pass) {
-                float v[32];
-                uint32_t pk[16];
-                const uint32_t at = buf + ((uint32_t)(16 * k) << 16);
-                tmem_ld_frag64(at + h * 64, v);
-                tmem_ld_wait();
-                fence_regs(v);
-                bool diagonal = false;  // (without item ids) a column equal to a row in this step
-                if constexpr (!HITS) {
-                    const int r0 = u.tile * K6_M + quarter * 32 + 16 * k, c0 = tt * TN + h * 64;
-                    diagonal = r0 < c0 + 64 && c0 < r0 + 16;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int4 c = cc[8 * h + e];
-                    const float2 bb = make_float2(__int_as_float(c.x), __int_as_float(c.z));
-                    float2 ww = make_float2(1.f, 1.f);
-                    if constexpr (decltype(pass)::value == 2) {
-                        const int j = tt * TN + h * 64 + 8 * e + col0;
-                        ww.x = j < cols ? __ldg(p.weight + j) : 0.f;
-                        ww.y = j + 1 < cols ? __ldg(p.weight + j + 1) : 0.f;
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float rb = rbias[2 * k + q];
-                        float2 x = fma2(make_float2(v[4 * e + 2 * q], v[4 * e + 2 * q + 1]), a2v, bb);
-                        x = add2(x, make_float2(rb, rb));
-                        if constexpr (HITS) {  // the diagonal among them
-                            x.x = c.y == rgrp[2 * k + q] ? -INFINITY : x.x;
-                            x.y = c.w == rgrp[2 * k + q] ? -INFINITY : x.y;
-                        } else if (diagonal) {
-                            const int i = row0 + 16 * k + 8 * q, j = tt * TN + h * 64 + 8 * e + col0;
-                            x.x = i == j ? -INFINITY : x.x;
-                            x.y = i == j + 1 ? -INFINITY : x.y;
-                        }
-                        float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                        if constexpr (decltype(pass)::value == 2) y = mul2(y, ww);
-                        pk[2 * e + q] = bf16x2_bits(y.x, y.y);
-                    }
-                }
-                tmem_st_frag32(at + h * 32, pk);
-            };
-            auto tile = [&](uint32_t buf, const int4 (&cc)[TN / 8], int tt, auto pass) {
-#pragma unroll
+            // A tile to P, in steps of 64 columns of one 16-row block. P of a step
+            // covers logits that the block's threads have read already. Loads and
+            // stores of 8 columns each: larger ones tie 32 registers into one
+            // operand, which the packed arithmetic then copies out of and into
+            // (1.5 moves per logit; 16384 x 32768 x 128 470 against 450 us).
+            // kind: bit 0 columns have weights; bit 1 (without item ids) a column
+            // may be a row.
+            auto tile = [&](uint32_t buf, const float* cs, int tt, auto kind) {
+                constexpr bool WEIGHTS = (decltype(kind)::value & 1) != 0, DIAGONAL = (decltype(kind)::value & 2) != 0;
+#pragma unroll 1
                 for (int h = 0; h < TN / 64; ++h) {
-                    step(buf, cc, tt, h, 0, pass);
-                    step(buf, cc, tt, h, 1, pass);
+                    f32x2 cb[8];
+                    int2 cg[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        cb[e] = *reinterpret_cast<const f32x2*>(cs + h * 64 + 8 * e + col0);
+                        if constexpr (HITS) cg[e] = *reinterpret_cast<const int2*>(cs + TN + h * 64 + 8 * e + col0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t at = buf + ((uint32_t)(16 * k) << 16);
+                        float v[32];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) tmem_ld_frag8(at + h * 64 + 8 * e, v + 4 * e);
+                        tmem_ld_wait();
+                        fence_regs(v);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const f32x2 acc = pair(v[4 * e + 2 * q], v[4 * e + 2 * q + 1]);
+                                float2 x = unpair(add2(fma2(acc, a2v, cb[e]), rbias[2 * k + q]));
+                                if constexpr (HITS) {  // the diagonal among them
+                                    x.x = cg[e].x == rgrp[2 * k + q] ? -INFINITY : x.x;
+                                    x.y = cg[e].y == rgrp[2 * k + q] ? -INFINITY : x.y;
+                                }
+                                if constexpr (DIAGONAL) {
+                                    const int i = row0 + 16 * k + 8 * q, j = tt * TN + h * 64 + 8 * e + col0;
+                                    x.x = i == j ? -INFINITY : x.x;
+                                    x.y = i == j + 1 ? -INFINITY : x.y;
+                                }
+                                float2 y = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                                if constexpr (WEIGHTS) {
+                                    const float2 ww = *reinterpret_cast<const float2*>(cs + 2 * TN + h * 64 + 8 * e + col0);
+                                    y.x *= ww.x;
+                                    y.y *= ww.y;
+                                }
+                                pk[2 * e + q] = bf16x2_bits(y.x, y.y);
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) tmem_st_frag4(at + h * 32 + 4 * e, pk[2 * e], pk[2 * e + 1]);
+                    }
                 }
             };
-            const int kind = u.pass == 0 || !p.weighted ? 1 : 2;
-            // first tile of this segment that is this group's
-            for (int t = t0 + (int)((K6_GROUPS + group - n % K6_GROUPS) % K6_GROUPS); t < t1; t += K6_GROUPS) {
-                const uint32_t nt = n + (uint32_t)(t - t0);
-                const int bf = nt % p.bufs;
-                int4 cc[TN / 8];
-                columns(cc, t);
-                if (!mbar_wait(&ctl->sfull[bf], (nt / p.bufs) & 1, abort)) { ok = false; break; }
+            const bool weights = u.pass == 1 && p.weighted;
+            // to the first tile of this segment that is this group's
+            int t = t0;
+            while (turn != group && t < t1) step_on(t);
+            while (t < t1) {
+                if (!mbar_wait(&ctl->sfull[bf.at], bf.phase, abort)) { ok = false; break; }
+                // the stage's column constants (complete before its logits were issued)
+                if (!mbar_wait(&ctl->full[st.at], st.phase, abort)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t buf = lane_base + acc_cols + (uint32_t)(bf * TN);
-                if (kind == 1) tile(buf, cc, t, Pass<1>{}); else tile(buf, cc, t, Pass<2>{});
+                const uint32_t buf = lane_base + acc_cols + (uint32_t)(bf.at * TN);
+                const float* cs = cols_sm + st.at * 3 * TN;
+                const bool diagonal = !HITS && t * TN < (u.tile + 1) * K6_M && u.tile * K6_M < (t + 1) * TN;
+                if (!diagonal) {
+                    if (weights) tile(buf, cs, t, Kind<1>{}); else tile(buf, cs, t, Kind<0>{});
+                } else if constexpr (!HITS) {
+                    if (weights) tile(buf, cs, t, Kind<3>{}); else tile(buf, cs, t, Kind<2>{});
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->pfull[bf]);
+                if (lane == 0) mbar_arrive(&ctl->pfull[bf.at]);
+#pragma unroll
+                for (int q = 0; q < K6_GROUPS; ++q)
+                    if (t < t1) step_on(t);
             }
             if (!ok) break;
             // the product of this segment
@@ -526,7 +558,6 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->accempty);
-            n += (uint32_t)(t1 - t0);
             w += t1 - t0;
         }
         if (!ok) {
@@ -553,51 +584,62 @@ struct K6Finish {
     const __nv_bfloat16 *users, *items;
     __nv_bfloat16 *grad_users, *grad_items;
     const int* err;
-    int b, nc, d, halves, width, grid;
+    int b, nc, d, width, grid;
     int64_t work;
     float inv_tau;
 };
 
-// A thread takes 8 columns of a row: of the users, then of the items.
+// A block takes 32 consecutive rows of one row tile (of the users, then of the
+// items) and one half of the columns; which parts of the line belong to the
+// tile is found once per block.
+constexpr int K6_FIN_ROWS = 32;
+
 template <int TN>
 __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
+    __shared__ int first, parts;
     const K6Line<TN> line(p.b, p.nc);
-    const int vpr = p.d / 8;
-    const int64_t total = ((int64_t)p.b + p.nc) * vpr;
-    const bool failed = *p.err != 0;
-    const float common = *p.common;
-    for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < total; v += (int64_t)gridDim.x * 256) {
-        const int64_t r = v / vpr;
-        const int col = (int)(v - r * vpr) * 8;
-        const int pass = r < p.b ? 0 : 1;
-        const int i = pass == 0 ? (int)r : (int)(r - p.b);
-        const int half = col / K6_HALF;
-        const int uid = half * (line.ru + line.rv) + (pass == 0 ? 0 : line.ru) + i / K6_M;
+    const int per_tile = K6_M / K6_FIN_ROWS;
+    const int q = blockIdx.x / per_tile;  // row tile
+    const int pass = q < line.ru ? 0 : 1;
+    const int half = blockIdx.y;
+    const int uid = half * (line.ru + line.rv) + q;
+    if (threadIdx.x == 0) {
         const K6Unit u = line.unit(uid);
-        // the blocks whose stretch of the line meets the unit's
-        int c = (int)((u.begin * p.grid) / p.work);
+        int c = (int)((u.begin * p.grid) / p.work);  // the block of k6_products that has the unit's first tile
         while (c > 0 && cta_begin(p.work, c, p.grid) > u.begin) --c;
         while (cta_begin(p.work, c + 1, p.grid) <= u.begin) ++c;
+        first = c;
+        while (c < p.grid && cta_begin(p.work, c, p.grid) < u.begin + u.cols) ++c;
+        parts = c - first;
+    }
+    __syncthreads();
+    const int row0 = (pass == 0 ? q : q - line.ru) * K6_M + (blockIdx.x % per_tile) * K6_FIN_ROWS;
+    const int rows = pass == 0 ? p.b : p.nc;
+    const int col0 = half * K6_HALF, cols = p.d - col0 < K6_HALF ? p.d - col0 : K6_HALF;
+    const bool failed = *p.err != 0;
+    const float common = pass == 1 ? *p.common : 1.f;
+    for (int v = threadIdx.x; v < K6_FIN_ROWS * (cols / 8); v += 256) {
+        const int r = v / (cols / 8), c8 = (v - r * (cols / 8)) * 8;
+        const int i = row0 + r;
+        if (i >= rows) break;
         float acc[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-        for (; c < p.grid && cta_begin(p.work, c, p.grid) < u.begin + u.cols; ++c) {
-            const float4* q = reinterpret_cast<const float4*>(
-                p.part + ((int64_t)(uid + c) * K6_M + i % K6_M) * p.width + (col - half * K6_HALF));
-            const float4 x = __ldg(q), y = __ldg(q + 1);
+        const float* src = p.part + ((int64_t)(uid + first) * K6_M + i % K6_M) * p.width + c8;
+#pragma unroll 4
+        for (int c = 0; c < parts; ++c, src += (int64_t)K6_M * p.width) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(src)), y = __ldg(reinterpret_cast<const float4*>(src) + 1);
             acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
             acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
         }
-        if (pass == 1) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) acc[k] *= common;
-        }
         const float w = i < p.b ? p.weight[i] : 0.f;
         float out[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = pass == 0 ? 0.f : acc[k] * common * p.inv_tau;
         if (w != 0.f) {
             Raw<__nv_bfloat16, 8> other;
             float x[8];
-            other.load((pass == 0 ? p.items : p.users) + (int64_t)i * p.d + col);
+            other.load((pass == 0 ? p.items : p.users) + (int64_t)i * p.d + col0 + c8);
             other.get(x);
             const float c_ii = p.diag[i];
             if (pass == 0) {
@@ -605,17 +647,14 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
                 for (int k = 0; k < 8; ++k) out[k] = fmaf(c_ii, x[k], acc[k]) * w * p.inv_tau;
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) out[k] = fmaf(c_ii * w, x[k], acc[k]) * p.inv_tau;
+                for (int k = 0; k < 8; ++k) out[k] = fmaf(c_ii * w, x[k], acc[k] * common) * p.inv_tau;
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) out[k] = pass == 0 ? 0.f : acc[k] * p.inv_tau;
         }
         if (failed) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) out[k] = NAN;
         }
-        store_row<8>((pass == 0 ? p.grad_users : p.grad_items) + (int64_t)i * p.d + col, out);
+        store_row<8>((pass == 0 ? p.grad_users : p.grad_items) + (int64_t)i * p.d + col0 + c8, out);
     }
 }
 
@@ -628,7 +667,7 @@ int log2_ceil(int64_t x) {
 template <int TN>
 int stages_for(int kchunks) {
     const int fixed = 1024 + kchunks * K6_M * 128 + (int)sizeof(K6Ctl);
-    const int s = (K6_SMEM_BUDGET - fixed) / (kchunks * TN * 128);
+    const int s = (K6_SMEM_BUDGET - fixed) / (kchunks * TN * 128 + TN * 12);
     return s < K6_MAX_STAGES ? s : K6_MAX_STAGES;
 }
 
@@ -666,9 +705,10 @@ SoftmaxGradPlan softmax_grad_plan(int b, int nc, int d, bool item_ids, bool copi
         return at;
     };
     pl.off_err = take(sizeof(int));  // first: tt_inbatch_softmax_check reads it at offset 0
-    pl.off_item = take((size_t)nc * sizeof(K6Side));
-    pl.off_user = take((size_t)b * sizeof(K6Side));
-    pl.off_weight = take((size_t)b * sizeof(float));
+    const size_t b_pad = ((size_t)b + K6_M - 1) / K6_M * K6_M, nc_pad = ((size_t)nc + K6_M - 1) / K6_M * K6_M;
+    pl.off_item = take(nc_pad * 8);  // biases, then groups
+    pl.off_user = take(b_pad * 8);
+    pl.off_weight = take(b_pad * sizeof(float));
     pl.off_diag = take((size_t)b * sizeof(float));
     pl.off_common = take(sizeof(float));
     pl.off_keys = take(item_ids ? ((size_t)1 << pl.log2_slots) * sizeof(unsigned long long) : 0);
@@ -683,9 +723,12 @@ namespace {
 
 template <int TN, bool HITS>
 cudaError_t launch_products(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, const K6Params& p, cudaStream_t s) {
-    const int smem = 1024 + p.kchunks * K6_M * 128 + p.stages * p.kchunks * TN * 128 + (int)sizeof(K6Ctl);
+    const int smem = 1024 + p.kchunks * K6_M * 128 + p.stages * (p.kchunks * TN * 128 + TN * 12) + (int)sizeof(K6Ctl);
     cudaError_t e = cudaFuncSetAttribute(k6_products<TN, HITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, k6_products<TN, HITS>)) != cudaSuccess) return e;
+    if (attr.numRegs * K6_THREADS < K6_SPLIT_REGS) return cudaErrorInvalidConfiguration;  // the register split would not fit
     note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
     k6_products<TN, HITS><<<pl.grid, K6_THREADS, smem, s>>>(g.tm_ux, g.tm_uy, g.tm_vx, g.tm_vy, p);
     note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
@@ -716,8 +759,11 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     q.grad_mean = g.grad_mean;
     q.keys = keys;
     q.log2_slots = pl.log2_slots;
-    q.item = reinterpret_cast<K6Side*>(ws + pl.off_item);
-    q.user = reinterpret_cast<K6Side*>(ws + pl.off_user);
+    const size_t b_pad = ((size_t)g.b + K6_M - 1) / K6_M * K6_M, nc_pad = ((size_t)g.nc + K6_M - 1) / K6_M * K6_M;
+    q.item.bias = reinterpret_cast<float*>(ws + pl.off_item);
+    q.item.grp = reinterpret_cast<int*>(q.item.bias + nc_pad);
+    q.user.bias = reinterpret_cast<float*>(ws + pl.off_user);
+    q.user.grp = reinterpret_cast<int*>(q.user.bias + b_pad);
     q.weight = reinterpret_cast<float*>(ws + pl.off_weight);
     q.diag = reinterpret_cast<float*>(ws + pl.off_diag);
     q.common = reinterpret_cast<float*>(ws + pl.off_common);
@@ -770,14 +816,13 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     f.b = g.b;
     f.nc = g.nc;
     f.d = g.d;
-    f.halves = pl.halves;
     f.width = pl.width;
     f.grid = pl.grid;
     f.work = pl.work;
     f.inv_tau = (float)(1.0 / (double)g.tau);
-    const int64_t blocks = (((int64_t)g.b + g.nc) * (g.d / 8) + 255) / 256;
+    const K6Line<TN> line(g.b, g.nc);
     note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
-    k6_finish<TN><<<(int)(blocks < 16 * sm_count ? blocks : 16 * sm_count), 256, 0, s>>>(f);
+    k6_finish<TN><<<dim3((unsigned)(line.ru + line.rv) * (K6_M / K6_FIN_ROWS), pl.halves), 256, 0, s>>>(f);
     note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
     return cudaGetLastError();
 }

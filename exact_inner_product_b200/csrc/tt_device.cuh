@@ -159,6 +159,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
         : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16) between 16-byte aligned addresses.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint64_t* bar, uint32_t bytes) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
 // Paired-CTA form: the copy lands in this CTA's shared memory and its bytes
 // are signalled on an mbarrier that may belong to the other CTA of the pair
 // (cluster address from mapa_shared). No multicast.
@@ -265,34 +273,21 @@ __device__ __forceinline__ void tmem_ld_wait() {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// 16 TMEM lanes x 64 fp32 columns over the warp, in the layout of a matrix
-// fragment: for each 8 columns i, v[4i], v[4i+1] are columns 8i + 2 (lane % 4)
-// and the next of TMEM lane (lane / 4), v[4i+2], v[4i+3] those of lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, float (&v)[32]) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+// 16 TMEM lanes x 8 fp32 columns over the warp, in the layout of a matrix
+// fragment: v[0], v[1] are columns 2 (lane % 4) and the next of TMEM lane
+// (lane / 4), v[2], v[3] those of lane / 4 + 8. Valid after tmem_ld_wait.
+__device__ __forceinline__ void tmem_ld_frag8(uint32_t taddr, float* v) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(taddr)
+                 : "memory");
 }
 
-// 16 TMEM lanes x 32 32-bit columns: for each 4 columns i, r[2i] is column
-// 4i + lane % 4 of TMEM lane (lane / 4), r[2i+1] that of lane / 4 + 8. With two
-// bf16 per register it holds what tmem_ld_frag64 read.
-__device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+// 16 TMEM lanes x 4 32-bit columns: r0 is column lane % 4 of TMEM lane
+// (lane / 4), r1 that of lane / 4 + 8. With two bf16 per register it holds what
+// tmem_ld_frag8 read.
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, uint32_t r0, uint32_t r1) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1, %2};" ::"r"(taddr), "r"(r0), "r"(r1) : "memory");
 }
 
 // Completes the thread's earlier tensor-memory stores.
