@@ -12,7 +12,8 @@
 // in fp32 at the end, so that the one large entry of a row is not rounded and
 // does not cancel.
 //
-// Kernels, in launch order:
+// Kernels, in launch order (each may start while the one before it still runs
+// and waits for its end before it touches memory; see pdl_wait):
 //   table_clear  (with item ids) empty the table that numbers the ids
 //   k6_prepare   per column: bias -log q_j log2(e), item group; per row:
 //                w_i, -lse_i log2(e) (-inf where w_i = 0), expm1(-loss_i);
@@ -96,6 +97,24 @@ struct K6Side {
     int* grp;
 };
 
+// The line of `work` tiles cut evenly among `grid` blocks: block c begins at
+// floor(work c / grid).
+struct K6Cut {
+    int64_t each;
+    int rest, grid;
+    K6Cut() = default;
+    K6Cut(int64_t work, int g) : each(work / g), rest((int)(work % g)), grid(g) {}
+    __device__ __forceinline__ int64_t begin(int c) const { return each * c + rest * c / grid; }
+    // the block that has tile w
+    __device__ __forceinline__ int block_of(int64_t w) const {
+        int c = (int)((double)w / ((double)each + (double)rest / grid));
+        if (c >= grid) c = grid - 1;
+        while (c > 0 && begin(c) > w) --c;
+        while (begin(c + 1) <= w) ++c;
+        return c;
+    }
+};
+
 struct K6Params {
     K6Side item;          // [nc]
     K6Side user;          // [b]
@@ -108,7 +127,7 @@ struct K6Params {
     int halves, width;    // products of `width` columns, in `halves` units
     int stages, bufs;
     int weighted;         // the items' pass multiplies P by w_i (else the rows' common weight is applied at the end)
-    int64_t work;         // tiles in all
+    K6Cut cut;
     uint32_t idesc_s;
 };
 
@@ -144,11 +163,6 @@ struct K6Line {
     }
 };
 
-__host__ __device__ __forceinline__ int64_t cta_begin(int64_t work, int cta, int grid) {
-    // work * cta may pass 64 bits only beyond 2^53 tiles
-    return work / grid * cta + work % grid * cta / grid;
-}
-
 // ---------------------------------------------------------------------------
 // preparation
 // ---------------------------------------------------------------------------
@@ -171,12 +185,19 @@ __global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
     __shared__ int valid_rows;
     const int tid = blockIdx.x * K6_PREP_THREADS + threadIdx.x;
     const int threads = gridDim.x * K6_PREP_THREADS;
-    if (tid == 0) *p.err = 0;
+    pdl_trigger();
     if (threadIdx.x == 0) valid_rows = 0;
     __syncthreads();
     if (p.valid != nullptr && p.grad_mean != nullptr) {  // every block counts all rows
         int n = 0;
-        for (int i = threadIdx.x; i < p.b; i += K6_PREP_THREADS) n += p.valid[i] != 0;
+        const bool words = (reinterpret_cast<uintptr_t>(p.valid) & 15) == 0;
+        const int whole = words ? p.b / 16 : 0;
+        auto set = [](uint32_t w) { return __popc(__vminu4(w, 0x01010101u)); };  // bytes that are not zero
+        for (int i = threadIdx.x; i < whole; i += K6_PREP_THREADS) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.valid) + i);
+            n += set(v.x) + set(v.y) + set(v.z) + set(v.w);
+        }
+        for (int i = 16 * whole + threadIdx.x; i < p.b; i += K6_PREP_THREADS) n += p.valid[i] != 0;
         n = __reduce_add_sync(0xffffffffu, n);
         if ((threadIdx.x & 31) == 0) atomicAdd(&valid_rows, n);
         __syncthreads();
@@ -184,6 +205,8 @@ __global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
     // the weight of every valid row, where there is no gradient per row
     const int count = p.valid != nullptr ? valid_rows : p.b;
     const float mean_w = p.grad_mean != nullptr && count > 0 ? *p.grad_mean / (float)count : 0.f;
+    pdl_wait();  // the empty table, and whoever used the workspace before
+    if (tid == 0) *p.err = 0;
     if (tid == 0) *p.common = p.grad_loss != nullptr ? 1.f : mean_w;
     // past the end, to whole tiles: columns without a share
     for (int j = p.nc + tid; j < (p.nc + K6_M - 1) / K6_M * K6_M; j += threads) {
@@ -258,8 +281,8 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const K6Line<TN> line(p.b, p.nc);
-    const int64_t w0 = cta_begin(p.work, blockIdx.x, gridDim.x);
-    const int64_t w1 = cta_begin(p.work, blockIdx.x + 1, gridDim.x);
+    const int64_t w0 = p.cut.begin(blockIdx.x);
+    const int64_t w1 = p.cut.begin(blockIdx.x + 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
@@ -288,6 +311,8 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
+    pdl_trigger();
+    pdl_wait();  // k6_prepare
     const uint32_t acc_cols = (uint32_t)((p.width + 31) / 32 * 32);  // the product; the logit tiles follow
     volatile int* abort = &ctl->abort;
 
@@ -584,8 +609,8 @@ struct K6Finish {
     const __nv_bfloat16 *users, *items;
     __nv_bfloat16 *grad_users, *grad_items;
     const int* err;
-    int b, nc, d, width, grid;
-    int64_t work;
+    int b, nc, d, width;
+    K6Cut cut;
     float inv_tau;
 };
 
@@ -598,6 +623,7 @@ template <int TN>
 __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
     __shared__ int first, parts;
     const K6Line<TN> line(p.b, p.nc);
+    pdl_trigger();
     const int per_tile = K6_M / K6_FIN_ROWS;
     const int q = blockIdx.x / per_tile;  // row tile
     const int pass = q < line.ru ? 0 : 1;
@@ -605,14 +631,13 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
     const int uid = half * (line.ru + line.rv) + q;
     if (threadIdx.x == 0) {
         const K6Unit u = line.unit(uid);
-        int c = (int)((u.begin * p.grid) / p.work);  // the block of k6_products that has the unit's first tile
-        while (c > 0 && cta_begin(p.work, c, p.grid) > u.begin) --c;
-        while (cta_begin(p.work, c + 1, p.grid) <= u.begin) ++c;
+        int c = p.cut.block_of(u.begin);
         first = c;
-        while (c < p.grid && cta_begin(p.work, c, p.grid) < u.begin + u.cols) ++c;
+        while (c < p.cut.grid && p.cut.begin(c) < u.begin + u.cols) ++c;
         parts = c - first;
     }
     __syncthreads();
+    pdl_wait();  // k6_products
     const int row0 = (pass == 0 ? q : q - line.ru) * K6_M + (blockIdx.x % per_tile) * K6_FIN_ROWS;
     const int rows = pass == 0 ? p.b : p.nc;
     const int col0 = half * K6_HALF, cols = p.d - col0 < K6_HALF ? p.d - col0 : K6_HALF;
@@ -730,9 +755,9 @@ cudaError_t launch_products(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, con
     if ((e = cudaFuncGetAttributes(&attr, k6_products<TN, HITS>)) != cudaSuccess) return e;
     if (attr.numRegs * K6_THREADS < K6_SPLIT_REGS) return cudaErrorInvalidConfiguration;  // the register split would not fit
     note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
-    k6_products<TN, HITS><<<pl.grid, K6_THREADS, smem, s>>>(g.tm_ux, g.tm_uy, g.tm_vx, g.tm_vy, p);
+    e = launch_pdl(k6_products<TN, HITS>, dim3(pl.grid), dim3(K6_THREADS), smem, s, g.tm_ux, g.tm_uy, g.tm_vx, g.tm_vy, p);
     note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
-    return cudaGetLastError();
+    return e;
 }
 
 template <int TN>
@@ -775,11 +800,18 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     q.nc = g.nc;
     q.vpr = g.d / 8;
     q.err = reinterpret_cast<int*>(ws + pl.off_err);
-    const int64_t prep = ((int64_t)g.nc + K6_PREP_THREADS - 1) / K6_PREP_THREADS;
+    // a thread per column, or per 16-byte piece to copy
+    const int64_t prep = ((int64_t)g.nc * (g.valid != nullptr ? q.vpr : 1) + K6_PREP_THREADS - 1) / K6_PREP_THREADS;
+    const dim3 prep_grid((unsigned)(prep < 4 * sm_count ? prep : 4 * sm_count));
     note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
-    k6_prepare<<<(int)(prep < 4 * sm_count ? prep : 4 * sm_count), K6_PREP_THREADS, 0, s>>>(q);
+    if (hits) {
+        e = launch_pdl(k6_prepare, prep_grid, dim3(K6_PREP_THREADS), 0, s, q);
+    } else {
+        k6_prepare<<<prep_grid, K6_PREP_THREADS, 0, s>>>(q);
+        e = cudaGetLastError();
+    }
     note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (e != cudaSuccess) return e;
 
     K6Params p;
     p.item = q.item;
@@ -797,7 +829,7 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     p.stages = pl.stages;
     p.bufs = pl.bufs;
     p.weighted = g.grad_loss != nullptr ? 1 : 0;
-    p.work = pl.work;
+    p.cut = K6Cut(pl.work, pl.grid);
     p.idesc_s = umma_idesc_bf16(K6_M, TN);
     e = hits ? launch_products<TN, true>(pl, g, p, s) : launch_products<TN, false>(pl, g, p, s);
     if (e != cudaSuccess) return e;
@@ -817,14 +849,13 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     f.nc = g.nc;
     f.d = g.d;
     f.width = pl.width;
-    f.grid = pl.grid;
-    f.work = pl.work;
+    f.cut = p.cut;
     f.inv_tau = (float)(1.0 / (double)g.tau);
     const K6Line<TN> line(g.b, g.nc);
     note_launch_begin(TT_KIND_SOFTMAX_GRAD, s);
-    k6_finish<TN><<<dim3((unsigned)(line.ru + line.rv) * (K6_M / K6_FIN_ROWS), pl.halves), 256, 0, s>>>(f);
+    e = launch_pdl(k6_finish<TN>, dim3((unsigned)(line.ru + line.rv) * (K6_M / K6_FIN_ROWS), pl.halves), dim3(256), 0, s, f);
     note_launch_end(TT_KIND_SOFTMAX_GRAD, s);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
