@@ -439,11 +439,14 @@ def tt_inbatch_softmax(users: torch.Tensor, items: torch.Tensor, tau: float = 1.
     return lse, loss, mean
 
 
-def _check_float(name: str, t: torch.Tensor, shape=None, dtypes=(torch.float32, torch.bfloat16), device=None):
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def _check_float(name: str, t: torch.Tensor, shape=None, dtypes=_FLOATS, device=None):
     """A contiguous CUDA tensor of one of ``dtypes`` (and of ``shape``, on ``device``)."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d)[6:] for d in dtypes)}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+    if not t.is_cuda or not t.is_contiguous() or (shape is not None and t.shape != shape):
         want = "" if shape is None else f" of shape {tuple(shape)}"
         raise ValueError(f"{name} must be a contiguous CUDA tensor{want}, got {tuple(t.shape)} on {t.device}")
     if device is not None and t.device != device:
