@@ -14,6 +14,7 @@ package raises ``ImportError``.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -163,13 +164,19 @@ def _dtype(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without a Stream object around it (0.1 against 3 us), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _options(path=0, rank_scale_pct=0, force_levels=0, cap=0, withhold_copy=0):
@@ -633,23 +640,28 @@ _ELEM = {torch.float32: TT_F32, torch.bfloat16: TT_BF16}
 
 
 def _tensor_list(name: str, tensors, like=None):
-    """Device pointers of contiguous float32/bfloat16 CUDA tensors, as a ctypes array."""
-    for i, t in enumerate(tensors):
-        if t.dtype not in _ELEM:
-            raise TypeError(f"{name}[{i}] must be float32 or bfloat16, got {t.dtype}")
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor")
-        if like is not None and (t.dtype != like[i].dtype or t.shape != like[i].shape):
-            raise ValueError(f"{name}[{i}] must have the dtype and shape of its gradient")
-    return (_vp * max(1, len(tensors)))(*[t.data_ptr() for t in tensors])
+    """Addresses of contiguous float32/bfloat16 CUDA tensors, as an array of 64-bit integers."""
+    good = all([t.is_cuda and t.is_contiguous() and t.dtype in _ELEM for t in tensors])
+    if good and like is not None:
+        good = all([t.dtype == o.dtype and t.shape == o.shape for t, o in zip(tensors, like)])
+    if not good:  # say which
+        for i, t in enumerate(tensors):
+            if t.dtype not in _ELEM:
+                raise TypeError(f"{name}[{i}] must be float32 or bfloat16, got {t.dtype}")
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor")
+            if like is not None and (t.dtype != like[i].dtype or t.shape != like[i].shape):
+                raise ValueError(f"{name}[{i}] must have the dtype and shape of its gradient")
+    return array.array("Q", [t.data_ptr() for t in tensors])
 
 
 def _norm_call(tensors, norm, workspace):
     tensors = list(tensors)
     count = len(tensors)
     ptrs = _tensor_list("grads", tensors)
-    n = (_i64 * max(1, count))(*[t.numel() for t in tensors])
-    dtypes = (_i32 * max(1, count))(*[_ELEM[t.dtype] for t in tensors])
+    n = array.array("q", [t.numel() for t in tensors])
+    dtypes = array.array("i", [_ELEM[t.dtype] for t in tensors])
+    n_at, dtypes_at = n.buffer_info()[0], dtypes.buffer_info()[0]
     dev = tensors[0].device if count else torch.device("cuda", torch.cuda.current_device())
     if norm is None:
         norm = torch.empty((), dtype=torch.float32, device=dev)
@@ -657,20 +669,22 @@ def _norm_call(tensors, norm, workspace):
         _check_float("norm", norm, (), (torch.float32,), dev)
     if workspace is None:
         need = ctypes.c_size_t(0)
-        _check(_lib.tt_clip_grad_norm_workspace(count, n, dtypes, ctypes.byref(need)), "tt_clip_grad_norm_workspace")
+        _check(_lib.tt_clip_grad_norm_workspace(count, n_at, dtypes_at, ctypes.byref(need)), "tt_clip_grad_norm_workspace")
         workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
     else:
         _check_float("workspace", workspace, dtypes=(torch.uint8,), device=dev)
-    return tensors, count, ptrs, n, dtypes, norm, workspace
+    # the arrays come along: their addresses are used
+    return tensors, count, ptrs, (n, n_at), (dtypes, dtypes_at), norm, workspace
 
 
 def tt_clip_grad_norm_workspace(grads) -> int:
     """Bytes of device workspace ``tt_grad_norm`` and ``tt_clip_grad_norm`` need for these tensors."""
     grads = list(grads)
     need = ctypes.c_size_t(0)
-    n = (_i64 * max(1, len(grads)))(*[t.numel() for t in grads])
-    dtypes = (_i32 * max(1, len(grads)))(*[_dtype(t) for t in grads])
-    _check(_lib.tt_clip_grad_norm_workspace(len(grads), n, dtypes, ctypes.byref(need)), "tt_clip_grad_norm_workspace")
+    n = array.array("q", [t.numel() for t in grads])
+    dtypes = array.array("i", [_dtype(t) for t in grads])
+    _check(_lib.tt_clip_grad_norm_workspace(len(grads), n.buffer_info()[0], dtypes.buffer_info()[0], ctypes.byref(need)),
+           "tt_clip_grad_norm_workspace")
     return int(need.value)
 
 
@@ -678,7 +692,7 @@ def tt_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tenso
     """The L2 norm of all elements of the tensors ``grads`` (float32 and
     bfloat16 may be mixed), as a float32 scalar on the device (``tt_grad_norm``)."""
     _, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace)
-    _check(_lib.tt_grad_norm(count, ptrs, n, dtypes, _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream)),
+    _check(_lib.tt_grad_norm(count, ptrs.buffer_info()[0], n[1], dtypes[1], _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream)),
            "tt_grad_norm")
     return norm
 
@@ -696,7 +710,8 @@ def tt_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | Non
         if len(out) != count:
             raise ValueError(f"out has {len(out)} tensors for {count} gradients")
         outs = _tensor_list("out", out, like=grads)
-    _check(_lib.tt_clip_grad_norm(count, ptrs, n, dtypes, outs, float(max_norm), _ptr(norm), _ptr(workspace),
+    _check(_lib.tt_clip_grad_norm(count, ptrs.buffer_info()[0], n[1], dtypes[1],
+                                  None if outs is None else outs.buffer_info()[0], float(max_norm), _ptr(norm), _ptr(workspace),
                                   workspace.numel(), _stream(stream)), "tt_clip_grad_norm")
     return norm
 

@@ -17,16 +17,17 @@
 //   k8_scatter     tiles, and every token to its place
 //   k8_heads,      (row form) which place of the output each run has
 //   k8_scan
-//   k8_runs        a warp adds 32 consecutive sorted tokens in fp32. A run that
-//                  lies inside is written; the part of one that crosses into
-//                  the next 32 goes to a partial row
-//   k8_join        the partial rows of each crossing run, in order
+//   k8_runs        a warp adds 32 consecutive sorted tokens in fp32, the block
+//                  joins what its eight warps hold of one run, and writes it; the
+//                  part of a run that reaches past the block goes to a partial row
+//   k8_join        the partial rows of each such run, in order
 // The order of every sum is fixed by the ids, so the bits repeat. Bound by the
 // reading of g (once, in rows) and, for few tokens, by the launches.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "tt_device.cuh"
 #include "tt_internal.h"
 #include "tt_rows.cuh"
 
@@ -103,8 +104,8 @@ constexpr int K8_SORT_THREADS = 256;
 constexpr int K8_SORT_WARPS = K8_SORT_THREADS / 32;
 constexpr int K8_KEYS = 16;                            // keys per thread
 constexpr int K8_TILE = K8_SORT_THREADS * K8_KEYS;     // 4096
-constexpr int K8_ONE_THREADS = 1024;
-constexpr int K8_ONE = K8_ONE_THREADS * K8_KEYS;       // 16384
+constexpr int K8_ONE = 512 * K8_KEYS;                  // most tokens of one block's sort
+constexpr int K8_ONE_SMALL = 256 * K8_KEYS;            // and of the smaller block's
 constexpr int K8_BINS = 256;
 constexpr int K8_RUN = 32;                             // sorted tokens of a warp
 constexpr int K8_RUN_WARPS = 8;
@@ -116,57 +117,56 @@ __device__ __forceinline__ uint32_t key_of(ID id, uint32_t rows) {
     return id >= 0 && (uint64_t)id < rows ? (uint32_t)id : rows;
 }
 
-// One digit of a tile held in registers (key k of warp w and round r is the
-// tile's element (w * K8_KEYS + r) * 32 + lane): cnt[w][v] becomes the number
-// of keys with digit v in warp w, rank[r] the number of equal digits before
-// the key in its warp. Keys past the end have digit >= bins.
-__device__ __forceinline__ void warp_ranks(const uint32_t* digit, uint32_t (*cnt)[K8_BINS], int* rank) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int v = lane; v < K8_BINS; v += 32) cnt[warp][v] = 0;
+// The place of a key: cnt (the warp's) holds where the next key of each digit
+// goes; lanes with the same digit follow in their order.
+__device__ __forceinline__ int warp_place(uint32_t digit, bool in, unsigned peers, uint32_t* cnt) {
+    const int before = __popc(peers & lanemask_lt());
+    const uint32_t at = in ? cnt[digit] : 0;
     __syncwarp();
-#pragma unroll
-    for (int r = 0; r < K8_KEYS; ++r) {
-        const bool in = digit[r] < K8_BINS;
-        const unsigned peers = __match_any_sync(0xffffffffu, digit[r]);
-        const int before = __popc(peers & ((1u << lane) - 1u));
-        const uint32_t old = in ? cnt[warp][digit[r]] : 0;
-        __syncwarp();
-        if (in && before == 0) cnt[warp][digit[r]] = old + __popc(peers);
-        __syncwarp();
-        rank[r] = (int)old + before;
-    }
+    if (in && before == 0) cnt[digit] = at + __popc(peers);
+    __syncwarp();
+    return (int)at + before;
 }
 
+// A token in the sort: its key and its place in the call's ids.
 struct SortArgs {
     const void* ids;       // first pass; null afterwards
-    const uint32_t* key_in;
-    const uint32_t* pos_in;
-    uint32_t* key_out;
-    uint32_t* pos_out;
+    const uint2* in;       // (key, token)
+    uint2* out;
     int32_t* hist;         // [K8_BINS][tiles]
     int32_t* total;        // [K8_BINS]
+    int* cross_count;      // zeroed by the first pass
     int64_t m;
     uint32_t rows;
     int tiles;
     int shift, bits;
+    __device__ __forceinline__ uint32_t digit(uint32_t key) const { return (key >> shift) & ((1u << bits) - 1u); }
 };
 
 template <typename ID>
-__device__ __forceinline__ uint32_t load_key(const SortArgs& a, int64_t i) {
-    return a.ids != nullptr ? key_of(__ldg(static_cast<const ID*>(a.ids) + i), a.rows) : __ldg(a.key_in + i);
+__device__ __forceinline__ uint2 load_token(const SortArgs& a, int64_t i) {
+    if (a.ids != nullptr) return make_uint2(key_of(__ldg(static_cast<const ID*>(a.ids) + i), a.rows), (uint32_t)i);
+    return __ldg(a.in + i);
 }
 
 template <typename ID>
 __global__ void __launch_bounds__(K8_SORT_THREADS) k8_count(const SortArgs a) {
     __shared__ int h[K8_BINS];
+    pdl_trigger();
     h[threadIdx.x] = 0;
     __syncthreads();
+    pdl_wait();
+    if (a.ids != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.cross_count = 0;
     const int64_t base = (int64_t)blockIdx.x * K8_TILE;
+    uint32_t key[K8_KEYS];
 #pragma unroll
     for (int r = 0; r < K8_KEYS; ++r) {
         const int64_t i = base + r * K8_SORT_THREADS + threadIdx.x;
-        if (i < a.m) atomicAdd(&h[(load_key<ID>(a, i) >> a.shift) & ((1u << a.bits) - 1u)], 1);
+        key[r] = i < a.m ? load_token<ID>(a, i).x : 0u;
     }
+#pragma unroll
+    for (int r = 0; r < K8_KEYS; ++r)
+        if (base + r * K8_SORT_THREADS + threadIdx.x < a.m) atomicAdd(&h[a.digit(key[r])], 1);
     __syncthreads();
     a.hist[(int64_t)threadIdx.x * a.tiles + blockIdx.x] = h[threadIdx.x];
 }
@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(K8_SORT_THREADS) k8_count(const SortArgs a) {
 // Block b: exclusive prefix of row b of x ([rows][len]), in place, and its sum.
 __global__ void __launch_bounds__(256) k8_scan(int32_t* __restrict__ x, int len, int32_t* __restrict__ total) {
     __shared__ int warp_tot[8];
+    pdl_trigger();
+    pdl_wait();
     int32_t* row = x + (int64_t)blockIdx.x * len;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int run = 0;
@@ -218,247 +220,309 @@ __device__ __forceinline__ int block_prefix256(int v, int* warp_tot) {
     return before + inc - v;
 }
 
+// The tile in the order of its digits in shared memory first, so that the
+// stores to the digits' places are of runs of consecutive tokens.
 template <typename ID>
 __global__ void __launch_bounds__(K8_SORT_THREADS) k8_scatter(const SortArgs a) {
+    __shared__ uint2 tile[K8_TILE];
     __shared__ uint32_t cnt[K8_SORT_WARPS][K8_BINS];
-    __shared__ int warp_tot[8];
+    __shared__ int to_out[K8_BINS];  // place in the output minus place in the tile, per digit
+    __shared__ int warp_tot[2][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t base = (int64_t)blockIdx.x * K8_TILE + (int64_t)warp * K8_KEYS * 32;
-    uint32_t key[K8_KEYS], digit[K8_KEYS];
-    int rank[K8_KEYS];
+    const int64_t first = (int64_t)blockIdx.x * K8_TILE;
+    const int64_t base = first + (int64_t)warp * K8_KEYS * 32;
+    pdl_trigger();
+    for (int v = lane; v < K8_BINS; v += 32) cnt[warp][v] = 0;
+    __syncwarp();
+    pdl_wait();
+    uint2 tok[K8_KEYS];
 #pragma unroll
     for (int r = 0; r < K8_KEYS; ++r) {
         const int64_t i = base + r * 32 + lane;
-        key[r] = i < a.m ? load_key<ID>(a, i) : 0u;
-        digit[r] = i < a.m ? (key[r] >> a.shift) & ((1u << a.bits) - 1u) : (uint32_t)K8_BINS;
+        tok[r] = i < a.m ? load_token<ID>(a, i) : make_uint2(0u, 0u);
     }
-    warp_ranks(digit, cnt, rank);
-    const int first = block_prefix256(__ldg(a.total + threadIdx.x), warp_tot);  // has a barrier
-    int at = first + __ldg(a.hist + (int64_t)threadIdx.x * a.tiles + blockIdx.x);
+#pragma unroll
+    for (int r = 0; r < K8_KEYS; ++r)
+        if (base + r * 32 + lane < a.m) atomicAdd(&cnt[warp][a.digit(tok[r].x)], 1u);
+    const int before = block_prefix256(__ldg(a.total + threadIdx.x), warp_tot[0]);  // has a barrier
+    int sum = 0;
 #pragma unroll
     for (int w = 0; w < K8_SORT_WARPS; ++w) {
         const int c = (int)cnt[w][threadIdx.x];
-        cnt[w][threadIdx.x] = (uint32_t)at;
-        at += c;
+        cnt[w][threadIdx.x] = (uint32_t)sum;
+        sum += c;
     }
+    const int local = block_prefix256(sum, warp_tot[1]);
+    to_out[threadIdx.x] = before + __ldg(a.hist + (int64_t)threadIdx.x * a.tiles + blockIdx.x) - local;
+#pragma unroll
+    for (int w = 0; w < K8_SORT_WARPS; ++w) cnt[w][threadIdx.x] += (uint32_t)local;
     __syncthreads();
+    unsigned peers[K8_KEYS];
+#pragma unroll
+    for (int r = 0; r < K8_KEYS; ++r)
+        peers[r] = __match_any_sync(0xffffffffu, base + r * 32 + lane < a.m ? a.digit(tok[r].x) : (uint32_t)K8_BINS);
 #pragma unroll
     for (int r = 0; r < K8_KEYS; ++r) {
-        const int64_t i = base + r * 32 + lane;
-        if (i >= a.m) continue;
-        const uint32_t to = cnt[warp][digit[r]] + (uint32_t)rank[r];
-        a.key_out[to] = key[r];
-        a.pos_out[to] = a.ids != nullptr ? (uint32_t)i : __ldg(a.pos_in + i);
+        const bool in = base + r * 32 + lane < a.m;
+        const int to = warp_place(a.digit(tok[r].x), in, peers[r], cnt[warp]);
+        if (in) tile[to] = tok[r];
+    }
+    __syncthreads();
+    const int here = a.m - first < K8_TILE ? (int)(a.m - first) : K8_TILE;
+    for (int i = threadIdx.x; i < here; i += K8_SORT_THREADS) {
+        const uint2 t = tile[i];
+        a.out[to_out[a.digit(t.x)] + i] = t;
     }
 }
 
 // All digits in one block: keys and places go from registers through shared
 // memory and back once per digit.
+template <int THREADS>
 struct OneSmem {
-    uint32_t key[K8_ONE];
-    uint16_t pos[K8_ONE];
-    uint32_t cnt[K8_ONE_THREADS / 32][K8_BINS];
-    int warp_tot[8];
-    int first[K8_BINS];
+    uint32_t key[2][THREADS * K8_KEYS];
+    uint16_t pos[2][THREADS * K8_KEYS];
+    uint32_t cnt[THREADS / 32][K8_BINS];
+    int warp_tot[32];
 };
 
-template <typename ID>
-__global__ void __launch_bounds__(K8_ONE_THREADS)
-    k8_sort_one(const ID* __restrict__ ids, int m, uint32_t rows, int passes, int bits, uint32_t* __restrict__ key_out,
-                uint32_t* __restrict__ pos_out) {
+// Block 0 sorts; the others set the `zeros` 16-byte pieces at `zero` (and the
+// last `tail` bytes), for the dense gradient's rows without a token.
+template <typename ID, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    k8_sort_one(const ID* __restrict__ ids, int m, uint32_t rows, int passes, int bits, uint2* __restrict__ out,
+                int* __restrict__ cross_count, uint4* __restrict__ zero, int64_t zeros, int tail) {
+    constexpr int PARTS = THREADS / K8_BINS;           // threads per digit
+    constexpr int PER = THREADS / 32 / PARTS;          // warps whose counts a thread adds
     extern __shared__ __align__(16) uint8_t raw[];
-    OneSmem& sm = *reinterpret_cast<OneSmem*>(raw);
+    OneSmem<THREADS>& sm = *reinterpret_cast<OneSmem<THREADS>*>(raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_trigger();
+    if (blockIdx.x > 0) {
+        const int64_t step = (int64_t)(gridDim.x - 1) * THREADS;
+        for (int64_t v = (int64_t)(blockIdx.x - 1) * THREADS + threadIdx.x; v < zeros; v += step)
+            zero[v] = make_uint4(0, 0, 0, 0);
+        if (blockIdx.x == 1 && threadIdx.x < tail) reinterpret_cast<uint8_t*>(zero + zeros)[threadIdx.x] = 0;
+        return;
+    }
+    if (threadIdx.x == 0) *cross_count = 0;
     // the warps share the m tokens evenly: a warp's tokens are consecutive
-    const int rounds = (m + K8_ONE_THREADS - 1) / K8_ONE_THREADS;
+    const int rounds = (m + THREADS - 1) / THREADS;
     const int base = warp * rounds * 32 + lane;
-    uint32_t key[K8_KEYS], digit[K8_KEYS];
-    uint16_t pos[K8_KEYS];
-    int rank[K8_KEYS];
-#pragma unroll
-    for (int r = 0; r < K8_KEYS; ++r) {
-        const int i = base + r * 32;
-        const bool in = r < rounds && i < m;
-        key[r] = in ? key_of(__ldg(ids + i), rows) : 0u;
-        pos[r] = (uint16_t)i;
+    for (int i = threadIdx.x; i < m; i += THREADS) {
+        sm.key[0][i] = key_of(__ldg(ids + i), rows);
+        sm.pos[0][i] = (uint16_t)i;
     }
+    const uint32_t mask = (1u << bits) - 1u;
+    uint32_t* cnt = sm.cnt[warp];
     for (int p = 0; p < passes; ++p) {
-        for (int v = lane; v < K8_BINS; v += 32) sm.cnt[warp][v] = 0;
-        __syncwarp();
+        const uint32_t* key = sm.key[p & 1];
+        const uint16_t* pos = sm.pos[p & 1];
+        const int shift = p * bits;
+        for (int v = lane; v < K8_BINS; v += 32) cnt[v] = 0;
+        __syncthreads();  // the keys are there
+#pragma unroll 4
+        for (int r = 0; r < rounds; ++r)
+            if (base + r * 32 < m) atomicAdd(cnt + (key[base + r * 32] >> shift & mask), 1u);
+        __syncthreads();
+        // the prefix over (digit, warp): PARTS threads per digit, PER warps each
+        const int v = threadIdx.x / PARTS, part = threadIdx.x % PARTS;
+        int c[PER], sum = 0;
 #pragma unroll
-        for (int r = 0; r < K8_KEYS; ++r) {
-            if (r >= rounds) break;
-            const bool in = base + r * 32 < m;
-            digit[r] = in ? (key[r] >> (p * bits)) & ((1u << bits) - 1u) : (uint32_t)K8_BINS;
-            const unsigned peers = __match_any_sync(0xffffffffu, digit[r]);
-            const int before = __popc(peers & ((1u << lane) - 1u));
-            const uint32_t old = in ? sm.cnt[warp][digit[r]] : 0;
-            __syncwarp();
-            if (in && before == 0) sm.cnt[warp][digit[r]] = old + __popc(peers);
-            __syncwarp();
-            rank[r] = (int)old + before;
+        for (int w = 0; w < PER; ++w) {
+            c[w] = (int)sm.cnt[part * PER + w][v];
+            sum += c[w];
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) sm.warp_tot[warp] = inc;
+        __syncthreads();
+        const int tot = lane < THREADS / 32 ? sm.warp_tot[lane] : 0;
+        int at = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? tot : 0);
+#pragma unroll
+        for (int w = 0; w < PER; ++w) {
+            sm.cnt[part * PER + w][v] = (uint32_t)at;
+            at += c[w];
         }
         __syncthreads();
-        int sum = 0;
-        if (threadIdx.x < K8_BINS) {
-#pragma unroll 8
-            for (int w = 0; w < K8_ONE_THREADS / 32; ++w) {
-                const int c = (int)sm.cnt[w][threadIdx.x];
-                sm.cnt[w][threadIdx.x] = (uint32_t)sum;
-                sum += c;
-            }
-            int inc = sum;
+        uint32_t* key_to = sm.key[(p & 1) ^ 1];
+        uint16_t* pos_to = sm.pos[(p & 1) ^ 1];
+        // lanes with the same digit: a vote per bit, of four rounds at once (on the
+        // many values of a digit __match_any_sync takes half as long again)
+        for (int r0 = 0; r0 < rounds; r0 += 4) {
+            uint32_t k[4];
+            unsigned peers[4];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
+            for (int q = 0; q < 4; ++q) {
+                const int i = base + (r0 + q) * 32;
+                const bool in = r0 + q < rounds && i < m;
+                k[q] = in ? key[i] >> shift : 0u;
+                peers[q] = __ballot_sync(0xffffffffu, in);
             }
-            if (lane == 31) sm.warp_tot[warp] = inc;
-            sm.first[threadIdx.x] = inc - sum;
+            for (int b = 0; b < bits; ++b) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const bool one = (k[q] >> b & 1u) != 0;
+                    const unsigned v = __ballot_sync(0xffffffffu, one);
+                    peers[q] &= one ? v : ~v;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int i = base + (r0 + q) * 32;
+                const bool in = r0 + q < rounds && i < m;
+                const int to = warp_place(k[q] & mask, in, peers[q], cnt);
+                if (in) {
+                    key_to[to] = key[i];
+                    pos_to[to] = pos[i];
+                }
+            }
         }
         __syncthreads();
-        if (threadIdx.x < K8_BINS) {
-            int before = 0;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) before += w < warp ? sm.warp_tot[w] : 0;
-            sm.first[threadIdx.x] += before;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < K8_KEYS; ++r) {
-            if (r < rounds && digit[r] < K8_BINS) {
-                const int to = sm.first[digit[r]] + (int)sm.cnt[warp][digit[r]] + rank[r];
-                sm.key[to] = key[r];
-                sm.pos[to] = pos[r];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < K8_KEYS; ++r) {
-            const int i = base + r * 32;
-            if (r < rounds && i < m) {
-                key[r] = sm.key[i];
-                pos[r] = sm.pos[i];
-            }
-        }
-        // the next pass's writes to sm.key come after two more barriers
     }
-#pragma unroll
-    for (int r = 0; r < K8_KEYS; ++r) {
-        const int i = base + r * 32;
-        if (r < rounds && i < m) {
-            key_out[i] = key[r];
-            pos_out[i] = pos[r];
-        }
-    }
+    for (int i = threadIdx.x; i < m; i += THREADS) out[i] = make_uint2(sm.key[passes & 1][i], sm.pos[passes & 1][i]);
 }
 
 // ---------------------------------------------------------------------------
 // the runs
 // ---------------------------------------------------------------------------
 struct RunArgs {
-    const uint32_t* key;   // [m] sorted
-    const uint32_t* pos;
+    const uint2* tok;      // [m] sorted (key, token)
     int64_t m;
     uint32_t rows;
     int d;
     float scale;
     int by_row;            // 1: output row = place of the run; 0: output row = id
     const int32_t* block_first;  // (by_row) runs before each block of k8_heads
-    int32_t* place;        // (by_row) [chunks] runs before the warp's 32 tokens, within that block
-    float* part;           // [chunks][2][d]
-    int2* cross;           // crossing runs: (chunk they begin in, output row)
+    int32_t* place;        // (by_row) [chunks] runs before a warp's 32 tokens, within that block
+    float* part;           // [blocks][2][d]
+    int2* cross;           // runs that go on past their block: (block, output row)
     int* cross_count;
-    int64_t chunks;
+    int64_t chunks;        // of 32 tokens
+    __device__ __forceinline__ uint32_t key(int64_t i) const { return __ldg(&tok[i].x); }
 };
 
 __device__ __forceinline__ bool is_head(const RunArgs& a, int64_t i) {
     if (i >= a.m) return false;
-    const uint32_t k = __ldg(a.key + i);
-    return k < a.rows && (i == 0 || __ldg(a.key + i - 1) != k);
+    const uint32_t k = a.key(i);
+    return k < a.rows && (i == 0 || a.key(i - 1) != k);
 }
 
 // Runs that begin in each 32 tokens: the prefix within the block's K8_HEADS
 // tokens, and the block's sum.
-__global__ void __launch_bounds__(128) k8_heads(const RunArgs a, int32_t* __restrict__ block_total) {
+constexpr int K8_HEADS_THREADS = 512;
+constexpr int K8_HEADS_CHUNKS = K8_HEADS / K8_RUN;
+
+__global__ void __launch_bounds__(K8_HEADS_THREADS) k8_heads(const RunArgs a, int32_t* __restrict__ block_total) {
+    constexpr int PER = K8_HEADS_CHUNKS / (K8_HEADS_THREADS / 32);
+    static_assert(K8_HEADS_CHUNKS == 128, "four warps scan the counts");
+    __shared__ int count[K8_HEADS_CHUNKS];
     __shared__ int warp_tot[4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    static_assert(K8_HEADS == 128 * K8_RUN, "one thread per warp-chunk");
     const int64_t base = (int64_t)blockIdx.x * K8_HEADS;
-    int mine = 0;  // thread t keeps the count of chunk t
-    for (int c = 0; c < 32; ++c) {
-        const int n = __popc(__ballot_sync(0xffffffffu, is_head(a, base + (warp * 32 + c) * K8_RUN + lane)));
-        if (lane == c) mine = n;
-    }
-    int inc = mine;
+    pdl_trigger();
+    pdl_wait();
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+    for (int c = 0; c < PER; ++c) {
+        const int n = __popc(__ballot_sync(0xffffffffu, is_head(a, base + (warp * PER + c) * K8_RUN + lane)));
+        if (lane == 0) count[warp * PER + c] = n;
     }
-    if (lane == 31) warp_tot[warp] = inc;
     __syncthreads();
+    int mine = 0, inc = 0;
+    if (warp < 4) {
+        inc = mine = count[threadIdx.x];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) warp_tot[warp] = inc;
+    }
+    __syncthreads();
+    if (warp >= 4) return;
     int before = 0;
     for (int w = 0; w < warp; ++w) before += warp_tot[w];
     const int64_t chunk = base / K8_RUN + threadIdx.x;
     if (chunk < a.chunks) a.place[chunk] = before + inc - mine;
-    if (threadIdx.x == 127) block_total[blockIdx.x] = before + inc;
+    if (threadIdx.x == K8_HEADS_CHUNKS - 1) block_total[blockIdx.x] = before + inc;
 }
+
+// What a warp's 32 tokens leave open, for the block to join.
+struct Open {
+    int head;      // its first run began before it
+    int through;   // and reaches past its end
+    int tail;      // a run that began here reaches past its end
+    int64_t row;   // that run's output row
+};
 
 template <typename T, typename TO, typename ID, int E>
 __global__ void __launch_bounds__(K8_RUN_WARPS * 32)
     k8_runs(const RunArgs a, const T* __restrict__ grad, TO* __restrict__ out, ID* __restrict__ out_ids) {
     constexpr int BATCH = 8;
-    const int lane = threadIdx.x & 31;
-    const int64_t chunk = (int64_t)blockIdx.x * K8_RUN_WARPS + (threadIdx.x >> 5);
-    if (chunk >= a.chunks) return;
+    __shared__ float sums[K8_RUN_WARPS][2][32 * E];  // of the open runs: head, tail
+    __shared__ Open open[K8_RUN_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t chunk = (int64_t)blockIdx.x * K8_RUN_WARPS + warp;
+    pdl_trigger();
+    pdl_wait();
     const int64_t i0 = chunk * K8_RUN;
     const int64_t i = i0 + lane;
-    const uint32_t key = i < a.m ? __ldg(a.key + i) : a.rows;
-    const uint32_t pos = i < a.m ? __ldg(a.pos + i) : 0u;
+    const uint2 tok = i < a.m ? __ldg(a.tok + i) : make_uint2(a.rows, 0u);
+    const uint32_t key = tok.x;
     uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
-    if (lane == 0) prev = i0 > 0 ? __ldg(a.key + i0 - 1) : a.rows;
-    const unsigned live = __ballot_sync(0xffffffffu, key < a.rows);
-    if (live == 0) return;
+    if (lane == 0) prev = i0 > 0 && i0 < a.m ? a.key(i0 - 1) : a.rows;
+    const int count = __popc(__ballot_sync(0xffffffffu, key < a.rows));  // those that count come first
     // bit q: token q begins a run (of those that count)
     const unsigned heads = __ballot_sync(0xffffffffu, key < a.rows && (prev != key || i == 0));
-    const int count = __popc(live);  // live tokens come first
     const uint32_t last_key = __shfl_sync(0xffffffffu, key, 31);
-    const bool goes_on = count == 32 && i0 + 32 < a.m && __ldg(a.key + i0 + 32) == last_key;
+    const bool goes_on = count == 32 && i0 + 32 < a.m && a.key(i0 + 32) == last_key;
     int64_t first = 0;  // place of the first run that begins here
-    if (a.by_row) first = (int64_t)__ldg(a.block_first + chunk / (K8_HEADS / K8_RUN)) + __ldg(a.place + chunk);
+    if (a.by_row && count > 0)
+        first = (int64_t)__ldg(a.block_first + chunk / K8_HEADS_CHUNKS) + __ldg(a.place + chunk);
     const int e = (blockIdx.y * 32 + lane) * E;
     const bool in = e < a.d;
     if (out_ids != nullptr && blockIdx.y == 0 && (heads >> lane & 1u))
         out_ids[first + __popc(heads & ((1u << lane) - 1u))] = (ID)key;
+    if (lane == 0) open[warp] = {0, 0, 0, 0};
     float acc[E];
 #pragma unroll
     for (int k = 0; k < E; ++k) acc[k] = 0.f;
     int begun = 0;  // runs begun so far
-    // write out the run that ends before token q
-    auto flush = [&](int q) {
-        const bool open = q == 32 && goes_on;
-        if (begun == 0) {  // began in an earlier chunk
-            if (in) store_row<E>(a.part + (chunk * 2) * a.d + e, acc);
-        } else {
-            const int64_t place = first + begun - 1;
-            const int64_t row = a.by_row ? place : (int64_t)__shfl_sync(0xffffffffu, key, q - 1);
-            if (open) {
-                if (in) store_row<E>(a.part + (chunk * 2 + 1) * a.d + e, acc);
-                if (lane == 0 && blockIdx.y == 0) a.cross[atomicAdd(a.cross_count, 1)] = make_int2((int)chunk, (int)row);
-            } else if (in) {
-                float y[E];
+    auto write_row = [&](int64_t row, const float* v) {
+        if (!in) return;
+        float y[E];
 #pragma unroll
-                for (int k = 0; k < E; ++k) y[k] = acc[k] * a.scale;
-                store_row<E>(out + row * a.d + e, y);
+        for (int k = 0; k < E; ++k) y[k] = v[k] * a.scale;
+        store_row<E>(out + row * a.d + e, y);
+    };
+    // the run that ends before token q
+    auto flush = [&](int q) {
+        const bool on = q == 32 && goes_on;
+        const int64_t row = a.by_row ? first + begun - 1 : (int64_t)__shfl_sync(0xffffffffu, key, q - 1);
+        if (begun == 0 || on) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) sums[warp][begun == 0 ? 0 : 1][lane * E + k] = acc[k];
+            if (lane == 0) {
+                if (begun == 0) {
+                    open[warp].head = 1;
+                    open[warp].through = on;
+                } else {
+                    open[warp].tail = 1;
+                    open[warp].row = row;
+                }
             }
+        } else {
+            write_row(row, acc);
         }
     };
     for (int b = 0; b < count; b += BATCH) {
         Raw<T, E> r[BATCH];
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
-            const uint32_t p = __shfl_sync(0xffffffffu, pos, b + q);
+            const uint32_t p = __shfl_sync(0xffffffffu, tok.y, b + q);
             if (in && b + q < count) r[q].load(grad + (int64_t)p * a.d + e); else r[q].zero();
         }
 #pragma unroll
@@ -476,15 +540,41 @@ __global__ void __launch_bounds__(K8_RUN_WARPS * 32)
             for (int k = 0; k < E; ++k) acc[k] += x[k];
         }
     }
-    flush(count);
+    if (count > 0) flush(count);
+    __syncthreads();
+    // Open runs within the block: the warp where one begins adds what the warps
+    // after it hold of it; warp 0 also does so for the one that reaches into the
+    // block. What reaches past the block becomes a partial row.
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const bool mine = which == 0 ? warp == 0 && open[0].head : open[warp].tail;
+        if (!mine) continue;
+        float s[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) s[k] = sums[warp][which][lane * E + k];
+        bool on = which == 0 ? open[0].through != 0 : true;
+        for (int w = warp + 1; on && w < K8_RUN_WARPS; ++w) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) s[k] += sums[w][0][lane * E + k];
+            on = open[w].through != 0;
+        }
+        if (which == 0 || on) {
+            if (in) store_row<E>(a.part + ((int64_t)blockIdx.x * 2 + which) * a.d + e, s);
+            if (which == 1 && lane == 0 && blockIdx.y == 0)
+                a.cross[atomicAdd(a.cross_count, 1)] = make_int2(blockIdx.x, (int)open[warp].row);
+        } else {
+            write_row(open[warp].row, s);
+        }
+    }
 }
 
-// A run that begins in chunk c and goes on: its own part row (slot 1 of c),
-// then slot 0 of the chunks after c that it reaches. A warp adds up to
-// K8_JOIN_WARP chunks; longer runs take the whole block, warp w the chunks
+// A run that begins in block c and goes on: its own partial row (slot 1 of c),
+// then slot 0 of the blocks after c that it reaches. A warp adds up to
+// K8_JOIN_WARP of them; longer runs take the whole block, warp w the blocks
 // c + 1 + w, c + 1 + w + 8, ..., and the warps' sums in order.
 constexpr int K8_JOIN_WARPS = 8;
-constexpr int K8_JOIN_WARP = 64;
+constexpr int K8_JOIN_WARP = 24;
+constexpr int K8_BLOCK = K8_RUN * K8_RUN_WARPS;  // tokens of a block of k8_runs
 
 template <int E>
 __device__ __forceinline__ void add_parts(const RunArgs& a, int64_t c, int64_t from, int64_t to, int step, int e,
@@ -512,17 +602,18 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
     __shared__ int64_t reach[K8_JOIN_WARPS];
     __shared__ float sums[K8_JOIN_WARPS][32 * E];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
     const int n = *a.cross_count;
     const int e = (blockIdx.y * 32 + lane) * E;
     const bool in = e < a.d;
     for (int b = blockIdx.x * K8_JOIN_WARPS; b < n; b += gridDim.x * K8_JOIN_WARPS) {
-        int64_t k = 0;  // chunks after the first that the run reaches
+        int64_t k = 0;  // blocks after the first that the run reaches
         if (b + warp < n) {
             const int64_t c = a.cross[b + warp].x;
-            const uint32_t key = __ldg(a.key + c * K8_RUN + K8_RUN - 1);
+            const uint32_t key = a.key(c * K8_BLOCK + K8_BLOCK - 1);
             while (true) {
-                const int64_t i = (c + 1 + k + lane) * K8_RUN;
-                const unsigned same = __ballot_sync(0xffffffffu, i < a.m && __ldg(a.key + i) == key);
+                const int64_t i = (c + 1 + k + lane) * K8_BLOCK;
+                const unsigned same = __ballot_sync(0xffffffffu, i < a.m && a.key(i) == key);
                 const int more = same == 0xffffffffu ? 32 : __ffs(~same) - 1;
                 k += more;
                 if (more < 32) break;
@@ -595,19 +686,18 @@ int run_elems(int d) {
 template <typename T, typename TO, typename ID, int E>
 cudaError_t runs_launch(const RunArgs& a, const void* grad, void* out, void* out_ids, cudaStream_t s, int sm_count) {
     const int cols = (a.d + 32 * E - 1) / (32 * E);
-    const dim3 grid((unsigned)((a.chunks + K8_RUN_WARPS - 1) / K8_RUN_WARPS), cols);
+    const int64_t blocks = (a.chunks + K8_RUN_WARPS - 1) / K8_RUN_WARPS;
     note_launch_begin(TT_KIND_EMBEDDING, s);
-    k8_runs<T, TO, ID, E><<<grid, K8_RUN_WARPS * 32, 0, s>>>(a, static_cast<const T*>(grad), static_cast<TO*>(out),
-                                                            static_cast<ID*>(out_ids));
+    cudaError_t e = launch_pdl(k8_runs<T, TO, ID, E>, dim3((unsigned)blocks, cols), dim3(K8_RUN_WARPS * 32), 0, s, a,
+                               static_cast<const T*>(grad), static_cast<TO*>(out), static_cast<ID*>(out_ids));
     note_launch_end(TT_KIND_EMBEDDING, s);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || a.chunks < 2) return e;  // nothing crosses
-    const int64_t most = (a.chunks + K8_JOIN_WARPS - 1) / K8_JOIN_WARPS;
+    if (e != cudaSuccess || blocks < 2) return e;  // nothing crosses
+    const int64_t most = (blocks + K8_JOIN_WARPS - 1) / K8_JOIN_WARPS;
     note_launch_begin(TT_KIND_EMBEDDING, s);
-    k8_join<TO, E><<<dim3((unsigned)(most < 4 * sm_count ? most : 4 * sm_count), cols), K8_JOIN_WARPS * 32, 0, s>>>(
-        a, static_cast<TO*>(out));
+    e = launch_pdl(k8_join<TO, E>, dim3((unsigned)(most < 4 * sm_count ? most : 4 * sm_count), cols),
+                   dim3(K8_JOIN_WARPS * 32), 0, s, a, static_cast<TO*>(out));
     note_launch_end(TT_KIND_EMBEDDING, s);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T, typename TO, typename ID>
@@ -621,15 +711,16 @@ cudaError_t runs_elems(const RunArgs& a, const void* grad, void* out, void* out_
 }
 
 struct GradPlan {
-    int64_t tiles, chunks, heads;
+    int64_t tiles, chunks, blocks, heads;
     int passes, bits;
-    size_t off_key[2], off_pos[2], off_hist, off_total, off_cross_count, off_cross, off_place, off_first, off_part, bytes;
+    size_t off_tok[2], off_hist, off_total, off_cross_count, off_cross, off_place, off_first, off_part, bytes;
 };
 
 GradPlan grad_plan(int64_t m, int64_t rows, int d) {
     GradPlan p;
     p.tiles = (m + K8_TILE - 1) / K8_TILE;
     p.chunks = (m + K8_RUN - 1) / K8_RUN;
+    p.blocks = (m + K8_BLOCK - 1) / K8_BLOCK;
     p.heads = (m + K8_HEADS - 1) / K8_HEADS;
     const int total = bit_length((uint32_t)rows);  // the key `rows` included
     p.passes = total > 0 ? (total + 7) / 8 : 1;
@@ -642,64 +733,75 @@ GradPlan grad_plan(int64_t m, int64_t rows, int d) {
         return at;
     };
     p.off_cross_count = take(sizeof(int));
-    for (int k = 0; k < 2; ++k) {
-        p.off_key[k] = take((size_t)m * 4);
-        p.off_pos[k] = take((size_t)m * 4);
-    }
+    for (int k = 0; k < 2; ++k) p.off_tok[k] = take((size_t)m * sizeof(uint2));
     p.off_hist = take((size_t)K8_BINS * p.tiles * 4);
     p.off_total = take(K8_BINS * 4);
-    p.off_cross = take((size_t)p.chunks * sizeof(int2));
+    p.off_cross = take((size_t)p.blocks * sizeof(int2));
     p.off_place = take((size_t)p.chunks * 4);
     p.off_first = take((size_t)p.heads * 4);
-    p.off_part = take((size_t)p.chunks * 2 * d * sizeof(float));
+    p.off_part = take((size_t)p.blocks * 2 * d * sizeof(float));
     p.bytes = off;
     return p;
 }
 
+// Sorts the tokens into *sorted. The sort of one block also sets `bytes` of
+// zeros at `zero`; the other one leaves that to the caller.
 template <typename ID>
-cudaError_t sort_tokens(const GradPlan& p, const void* ids, int64_t m, uint32_t rows, uint8_t* ws, cudaStream_t s,
-                        int* which) {
-    uint32_t* key[2] = {reinterpret_cast<uint32_t*>(ws + p.off_key[0]), reinterpret_cast<uint32_t*>(ws + p.off_key[1])};
-    uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(ws + p.off_pos[0]), reinterpret_cast<uint32_t*>(ws + p.off_pos[1])};
+cudaError_t sort_tokens(const GradPlan& p, const void* ids, int64_t m, uint32_t rows, uint8_t* ws, void* zero,
+                        size_t bytes, cudaStream_t s, int sm_count, const uint2** sorted) {
+    uint2* tok[2] = {reinterpret_cast<uint2*>(ws + p.off_tok[0]), reinterpret_cast<uint2*>(ws + p.off_tok[1])};
+    int* cross_count = reinterpret_cast<int*>(ws + p.off_cross_count);
     cudaError_t e;
     if (m <= K8_ONE) {
-        *which = 0;
-        e = cudaFuncSetAttribute(k8_sort_one<ID>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(OneSmem));
-        if (e != cudaSuccess) return e;
-        note_launch_begin(TT_KIND_EMBEDDING, s);
-        k8_sort_one<ID><<<1, K8_ONE_THREADS, sizeof(OneSmem), s>>>(static_cast<const ID*>(ids), (int)m, rows, p.passes,
-                                                                  p.bits, key[0], pos[0]);
-        note_launch_end(TT_KIND_EMBEDDING, s);
-        return cudaGetLastError();
+        *sorted = tok[0];
+        const int threads = m <= K8_ONE_SMALL ? 256 : 512;
+        const int64_t fill = ((int64_t)(bytes / 16) + threads - 1) / threads;
+        const int grid = bytes == 0 ? 1 : 1 + (int)(fill < 1 ? 1 : fill < sm_count - 1 ? fill : sm_count - 1);
+        auto launch = [&](auto kernel, size_t smem) {
+            if (smem > 48 * 1024 &&
+                (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+                return e;
+            note_launch_begin(TT_KIND_EMBEDDING, s);
+            kernel<<<grid, threads, smem, s>>>(static_cast<const ID*>(ids), (int)m, rows, p.passes, p.bits, tok[0],
+                                               cross_count, static_cast<uint4*>(zero), (int64_t)(bytes / 16),
+                                               (int)(bytes % 16));
+            note_launch_end(TT_KIND_EMBEDDING, s);
+            return cudaGetLastError();
+        };
+        return threads == 256 ? launch(k8_sort_one<ID, 256>, sizeof(OneSmem<256>))
+                              : launch(k8_sort_one<ID, 512>, sizeof(OneSmem<512>));
     }
     SortArgs a;
     a.hist = reinterpret_cast<int32_t*>(ws + p.off_hist);
     a.total = reinterpret_cast<int32_t*>(ws + p.off_total);
+    a.cross_count = cross_count;
     a.m = m;
     a.rows = rows;
     a.tiles = (int)p.tiles;
     a.bits = p.bits;
     for (int q = 0; q < p.passes; ++q) {
-        const int to = q & 1;
         a.ids = q == 0 ? ids : nullptr;
-        a.key_in = key[to ^ 1];
-        a.pos_in = pos[to ^ 1];
-        a.key_out = key[to];
-        a.pos_out = pos[to];
+        a.in = tok[(q & 1) ^ 1];
+        a.out = tok[q & 1];
         a.shift = q * p.bits;
         note_launch_begin(TT_KIND_EMBEDDING, s);
-        k8_count<ID><<<a.tiles, K8_SORT_THREADS, 0, s>>>(a);
+        if (q == 0) {
+            k8_count<ID><<<a.tiles, K8_SORT_THREADS, 0, s>>>(a);
+            e = cudaGetLastError();
+        } else {
+            e = launch_pdl(k8_count<ID>, dim3(a.tiles), dim3(K8_SORT_THREADS), 0, s, a);
+        }
         note_launch_end(TT_KIND_EMBEDDING, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
         note_launch_begin(TT_KIND_EMBEDDING, s);
-        k8_scan<<<K8_BINS, 256, 0, s>>>(a.hist, a.tiles, a.total);
+        e = launch_pdl(k8_scan, dim3(1 << p.bits), dim3(256), 0, s, a.hist, a.tiles, a.total);
         note_launch_end(TT_KIND_EMBEDDING, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
         note_launch_begin(TT_KIND_EMBEDDING, s);
-        k8_scatter<ID><<<a.tiles, K8_SORT_THREADS, 0, s>>>(a);
+        e = launch_pdl(k8_scatter<ID>, dim3(a.tiles), dim3(K8_SORT_THREADS), 0, s, a);
         note_launch_end(TT_KIND_EMBEDDING, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        *which = to;
+        if (e != cudaSuccess) return e;
+        *sorted = a.out;
     }
     return cudaSuccess;
 }
@@ -709,18 +811,12 @@ cudaError_t embedding_grad_ids(const EmbeddingGrad& g, bool by_row, cudaStream_t
     uint8_t* ws = static_cast<uint8_t*>(g.workspace);
     const GradPlan p = grad_plan(g.m, g.rows, g.d);
     cudaError_t e;
-    if (!by_row) {
-        const size_t bytes = (size_t)g.rows * g.d * (g.out_dtype == TT_F32 ? 4 : 2);
-        if (bytes > 0 && (e = cudaMemsetAsync(g.out, 0, bytes, s)) != cudaSuccess) return e;
-    }
+    const size_t zeros = by_row ? 0 : (size_t)g.rows * g.d * (g.out_dtype == TT_F32 ? 4 : 2);
+    if (zeros > 0 && (g.m > K8_ONE || g.m == 0) && (e = cudaMemsetAsync(g.out, 0, zeros, s)) != cudaSuccess) return e;
     if (g.m == 0) return by_row ? cudaMemsetAsync(g.count, 0, sizeof(int32_t), s) : cudaSuccess;
-    int* cross_count = reinterpret_cast<int*>(ws + p.off_cross_count);
-    if ((e = cudaMemsetAsync(cross_count, 0, sizeof(int), s)) != cudaSuccess) return e;
-    int which = 0;
-    if ((e = sort_tokens<ID>(p, g.ids, g.m, (uint32_t)g.rows, ws, s, &which)) != cudaSuccess) return e;
     RunArgs a;
-    a.key = reinterpret_cast<uint32_t*>(ws + p.off_key[which]);
-    a.pos = reinterpret_cast<uint32_t*>(ws + p.off_pos[which]);
+    if ((e = sort_tokens<ID>(p, g.ids, g.m, (uint32_t)g.rows, ws, g.out, zeros, s, sm_count, &a.tok)) != cudaSuccess)
+        return e;
     a.m = g.m;
     a.rows = (uint32_t)g.rows;
     a.d = g.d;
@@ -731,17 +827,17 @@ cudaError_t embedding_grad_ids(const EmbeddingGrad& g, bool by_row, cudaStream_t
     a.place = reinterpret_cast<int32_t*>(ws + p.off_place);
     a.part = reinterpret_cast<float*>(ws + p.off_part);
     a.cross = reinterpret_cast<int2*>(ws + p.off_cross);
-    a.cross_count = cross_count;
+    a.cross_count = reinterpret_cast<int*>(ws + p.off_cross_count);
     a.chunks = p.chunks;
     if (by_row) {
         note_launch_begin(TT_KIND_EMBEDDING, s);
-        k8_heads<<<(unsigned)p.heads, 128, 0, s>>>(a, first);
+        e = launch_pdl(k8_heads, dim3((unsigned)p.heads), dim3(K8_HEADS_THREADS), 0, s, a, first);
         note_launch_end(TT_KIND_EMBEDDING, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
         note_launch_begin(TT_KIND_EMBEDDING, s);
-        k8_scan<<<1, 256, 0, s>>>(first, (int)p.heads, g.count);
+        e = launch_pdl(k8_scan, dim3(1), dim3(256), 0, s, first, (int)p.heads, g.count);
         note_launch_end(TT_KIND_EMBEDDING, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
     }
     if (g.grad_dtype == TT_F32)
         return g.out_dtype == TT_F32
