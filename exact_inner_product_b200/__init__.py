@@ -15,6 +15,7 @@ package raises ``ImportError``.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
 
@@ -177,6 +178,15 @@ def _stream(stream):
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+_NO_STREAM = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call makes its tensors: on the stream it runs on, so that memory
+    that is freed again (a workspace) is reused after the call's kernels."""
+    return _NO_STREAM if stream is None else torch.cuda.stream(stream)
 
 
 def _options(path=0, rank_scale_pct=0, force_levels=0, cap=0, withhold_copy=0):
@@ -460,9 +470,10 @@ def _check_float(name: str, t: torch.Tensor, shape=None, dtypes=_FLOATS, device=
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _workspace(workspace, need: int, device):
+def _workspace(workspace, need: int, device, stream):
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        with _on(stream):
+            return torch.empty(need, dtype=torch.uint8, device=device)
     _check_float("workspace", workspace, dtypes=(torch.uint8,), device=device)
     return workspace
 
@@ -484,8 +495,9 @@ def tt_layernorm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torc
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError("weight and bias must have one dtype")
     if out is None:
-        out = (torch.empty_like(x), torch.empty(n, dtype=torch.float32, device=dev),
-               torch.empty(n, dtype=torch.float32, device=dev))
+        with _on(stream):
+            out = (torch.empty_like(x), torch.empty(n, dtype=torch.float32, device=dev),
+                   torch.empty(n, dtype=torch.float32, device=dev))
     else:
         _check_float("out y", out[0], (n, d), (x.dtype,), dev)
         _check_float("out mean", out[1], (n,), (torch.float32,), dev)
@@ -522,14 +534,15 @@ def tt_layernorm_grad(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     _check_float("mean", mean, (n,), (torch.float32,), dev)
     _check_float("rstd", rstd, (n,), (torch.float32,), dev)
     if out is None:
-        out = (torch.empty_like(x), torch.empty(d, dtype=torch.float32, device=dev),
-               torch.empty(d, dtype=torch.float32, device=dev))
+        with _on(stream):
+            out = (torch.empty_like(x), torch.empty(d, dtype=torch.float32, device=dev),
+                   torch.empty(d, dtype=torch.float32, device=dev))
     else:
         for name, t, shape, dt in (("out grad_x", out[0], (n, d), x.dtype), ("out grad_weight", out[1], (d,), torch.float32),
                                    ("out grad_bias", out[2], (d,), torch.float32)):
             if t is not None:
                 _check_float(name, t, shape, (dt,), dev)
-    workspace = _workspace(workspace, tt_layernorm_grad_workspace(n, d) if workspace is None else 0, dev)
+    workspace = _workspace(workspace, tt_layernorm_grad_workspace(n, d) if workspace is None else 0, dev, stream)
     _check(_lib.tt_layernorm_grad(_ptr(grad_y), _ptr(x), _dtype(x), n, d, _ptr(weight),
                                   TT_F32 if weight is None else _dtype(weight), _ptr(mean), _ptr(rstd), _ptr(out[0]),
                                   _ptr(out[1]), _ptr(out[2]), _ptr(workspace), workspace.numel(), _stream(stream)),
@@ -547,7 +560,8 @@ def tt_normalize_grad(grad_y: torch.Tensor, x: torch.Tensor, out: torch.Tensor |
     _check_float("grad_y", grad_y, x.shape, device=x.device)
     n, d = x.shape
     if out is None:
-        out = torch.empty_like(x)
+        with _on(stream):
+            out = torch.empty_like(x)
     else:
         _check_float("out", out, x.shape, (x.dtype,), x.device)
     _check(_lib.tt_normalize_grad(_ptr(grad_y), _dtype(grad_y), _ptr(x), _dtype(x), n, d, _ptr(out), _stream(stream)),
@@ -570,7 +584,8 @@ def tt_embedding(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, out
     _check_float("ids", ids, dtypes=_IDS, device=table.device)
     rows, d = table.shape
     if out is None:
-        out = torch.empty((*ids.shape, d), dtype=out_dtype or table.dtype, device=table.device)
+        with _on(stream):
+            out = torch.empty((*ids.shape, d), dtype=out_dtype or table.dtype, device=table.device)
     _check_float("out", out, (*ids.shape, d), (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,),
                  table.device)
     _check(_lib.tt_embedding(_ptr(table), _dtype(table), rows, d, _ptr(ids), ids.element_size(), ids.numel(),
@@ -586,13 +601,14 @@ def tt_embedding_grad_workspace(m: int, rows: int, d: int) -> int:
     return int(need.value)
 
 
-def _embedding_grad_args(ids, grad, rows, workspace):
+def _embedding_grad_args(ids, grad, rows, workspace, stream):
     if grad.dim() < 1 or grad.shape[:-1] != ids.shape:
         raise ValueError(f"grad must be [*ids.shape, d], got {tuple(grad.shape)} for ids {tuple(ids.shape)}")
     _check_float("grad", grad)
     _check_float("ids", ids, dtypes=_IDS, device=grad.device)
     m, d = ids.numel(), grad.shape[-1]
-    return m, d, _workspace(workspace, tt_embedding_grad_workspace(m, rows, d) if workspace is None else 0, grad.device)
+    need = tt_embedding_grad_workspace(m, rows, d) if workspace is None else 0
+    return m, d, _workspace(workspace, need, grad.device, stream)
 
 
 def tt_embedding_grad(ids: torch.Tensor, grad: torch.Tensor, rows: int, scale: float = 1.0,
@@ -601,9 +617,10 @@ def tt_embedding_grad(ids: torch.Tensor, grad: torch.Tensor, rows: int, scale: f
     """The gradient of ``tt_embedding`` with respect to the table
     (``tt_embedding_grad``): ``grad`` is [*ids.shape, d]. Returns [rows, d] in
     ``out_dtype`` (default: grad's), zeros where no id points."""
-    m, d, workspace = _embedding_grad_args(ids, grad, rows, workspace)
+    m, d, workspace = _embedding_grad_args(ids, grad, rows, workspace, stream)
     if out is None:
-        out = torch.empty((rows, d), dtype=out_dtype or grad.dtype, device=grad.device)
+        with _on(stream):
+            out = torch.empty((rows, d), dtype=out_dtype or grad.dtype, device=grad.device)
     _check_float("out", out, (rows, d), (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,),
                  grad.device)
     _check(_lib.tt_embedding_grad(_ptr(ids), ids.element_size(), m, _ptr(grad), _dtype(grad), int(rows), d, float(scale),
@@ -620,15 +637,17 @@ def tt_embedding_grad_rows(ids: torch.Tensor, grad: torch.Tensor, rows: int, sca
     with m = ids.numel(). The first ``count`` entries hold the ids, ascending,
     and their rows; what lies behind them is left as it was. ``out`` gives the
     first two tensors."""
-    m, d, workspace = _embedding_grad_args(ids, grad, rows, workspace)
+    m, d, workspace = _embedding_grad_args(ids, grad, rows, workspace, stream)
     dev = grad.device
     if out is None:
-        out = (torch.empty(m, dtype=ids.dtype, device=dev),
-               torch.empty((m, d), dtype=out_dtype or grad.dtype, device=dev))
+        with _on(stream):
+            out = (torch.empty(m, dtype=ids.dtype, device=dev),
+                   torch.empty((m, d), dtype=out_dtype or grad.dtype, device=dev))
     _check_float("out ids", out[0], (m,), (ids.dtype,), dev)
     _check_float("out rows", out[1], (m, d), (torch.float32, torch.bfloat16) if out_dtype is None else (out_dtype,), dev)
     if count is None:
-        count = torch.empty(1, dtype=torch.int32, device=dev)
+        with _on(stream):
+            count = torch.empty(1, dtype=torch.int32, device=dev)
     _check_float("count", count, (1,), (torch.int32,), dev)
     _check(_lib.tt_embedding_grad_rows(_ptr(ids), ids.element_size(), m, _ptr(grad), _dtype(grad), int(rows), d,
                                        float(scale), _ptr(out[0]), _ptr(out[1]), _dtype(out[1]), _ptr(count),
@@ -655,7 +674,7 @@ def _tensor_list(name: str, tensors, like=None):
     return array.array("Q", [t.data_ptr() for t in tensors])
 
 
-def _norm_call(tensors, norm, workspace):
+def _norm_call(tensors, norm, workspace, stream):
     tensors = list(tensors)
     count = len(tensors)
     ptrs = _tensor_list("grads", tensors)
@@ -664,13 +683,15 @@ def _norm_call(tensors, norm, workspace):
     n_at, dtypes_at = n.buffer_info()[0], dtypes.buffer_info()[0]
     dev = tensors[0].device if count else torch.device("cuda", torch.cuda.current_device())
     if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
+        with _on(stream):
+            norm = torch.empty((), dtype=torch.float32, device=dev)
     else:
         _check_float("norm", norm, (), (torch.float32,), dev)
     if workspace is None:
         need = ctypes.c_size_t(0)
         _check(_lib.tt_clip_grad_norm_workspace(count, n_at, dtypes_at, ctypes.byref(need)), "tt_clip_grad_norm_workspace")
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
+        with _on(stream):
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
     else:
         _check_float("workspace", workspace, dtypes=(torch.uint8,), device=dev)
     # the arrays come along: their addresses are used
@@ -691,7 +712,7 @@ def tt_clip_grad_norm_workspace(grads) -> int:
 def tt_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """The L2 norm of all elements of the tensors ``grads`` (float32 and
     bfloat16 may be mixed), as a float32 scalar on the device (``tt_grad_norm``)."""
-    _, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace)
+    _, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace, stream)
     _check(_lib.tt_grad_norm(count, ptrs.buffer_info()[0], n[1], dtypes[1], _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream)),
            "tt_grad_norm")
     return norm
@@ -703,7 +724,7 @@ def tt_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | Non
     ``max_norm`` (``tt_clip_grad_norm``): in place, or into the tensors of
     ``out``. Returns the norm before the scaling, a float32 scalar on the
     device; nothing is read back to the host."""
-    grads, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace)
+    grads, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace, stream)
     outs = None
     if out is not None:
         out = list(out)
@@ -763,9 +784,10 @@ def tt_inbatch_softmax_grad(users: torch.Tensor, items: torch.Tensor, lse: torch
     need = 0
     if workspace is None:
         need = tt_inbatch_softmax_grad_workspace(b, nc, d, item_ids is not None, valid is not None)
-    workspace = _workspace(workspace, need, dev)
+    workspace = _workspace(workspace, need, dev, stream)
     if out is None:
-        out = (torch.empty_like(users), torch.empty_like(items))
+        with _on(stream):
+            out = (torch.empty_like(users), torch.empty_like(items))
     else:
         _check_float("out grad_users", out[0], (b, d), (users.dtype,), dev)
         _check_float("out grad_items", out[1], (nc, d), (users.dtype,), dev)

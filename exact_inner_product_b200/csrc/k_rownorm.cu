@@ -28,7 +28,7 @@
 // thread's columns, stay the same from row to row: the column sums stay in
 // registers, and the thread's weights, loaded once, in its own shared memory
 // (element by element, 100000 x 777 bf16 took 432 us forward and 602 us back; so
-// 169 and 270).
+// 169 and 256).
 //
 // The column sums dw and dbias: each thread keeps its columns' sums in
 // registers over all the rows it handles, the block adds its warps' sums in
@@ -48,7 +48,15 @@ namespace {
 
 constexpr int K7_THREADS = 256;
 constexpr int K7_WARPS = K7_THREADS / 32;
-constexpr int K7_GRAD_BLOCKS = 2;  // per SM: the gradient's registers hold two sums per column
+
+// The gradient's blocks: its threads hold two sums per column, and with the row
+// at hand and the next one on its way that is 128 registers and more for CH = 4
+// chunks, so those blocks have 12 warps and one fits an SM (65536 x 1000 bf16:
+// 16 warps that wait for their loads 105 us, 12 that have them ahead 82 us).
+template <int CH>
+constexpr int grad_warps() { return CH >= 4 ? 12 : K7_WARPS; }
+template <int CH>
+constexpr int grad_resident() { return CH >= 4 ? 1 : 2; }
 
 __device__ __forceinline__ float sum2(f32x2 a) {
     const float2 v = unpair(a);
@@ -148,7 +156,7 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2 (*sm)[32],
 }
 
 // Who shares a row: L lanes of a warp (L > 0), or the block (L = 0).
-template <int L>
+template <int L, int WARPS = K7_WARPS>
 struct Group {
     int lane, size, turn;
     int64_t row, step;  // the group's first row, and the distance to its next
@@ -156,8 +164,8 @@ struct Group {
         if constexpr (L > 0) {
             lane = threadIdx.x & (L - 1);
             size = L;
-            row = ((int64_t)blockIdx.x * K7_WARPS + (threadIdx.x >> 5)) * (32 / L) + (threadIdx.x & 31) / L;
-            step = (int64_t)gridDim.x * K7_WARPS * (32 / L);
+            row = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * (32 / L) + (threadIdx.x & 31) / L;
+            step = (int64_t)gridDim.x * WARPS * (32 / L);
         } else {
             lane = threadIdx.x;
             size = blockDim.x;
@@ -310,14 +318,15 @@ __global__ void __launch_bounds__(L > 0 ? K7_THREADS : 512)
 }
 
 template <typename T, typename TW, int L, int CH, bool ALIGNED>
-__global__ void __launch_bounds__(L > 0 ? K7_THREADS : 512, L > 0 ? K7_GRAD_BLOCKS : 1)
+__global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? grad_resident<CH>() : 1)
     k7_layernorm_grad(const T* __restrict__ dy, const T* __restrict__ x, const TW* __restrict__ w,
                       const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* __restrict__ dx,
                       float* __restrict__ part, int64_t n, int d) {
-    constexpr bool AHEAD = CH <= 2;  // beyond that the registers are needed for the sums
+    constexpr bool AHEAD = L > 0 || CH <= 2;
+    constexpr int WARPS = grad_warps<CH>();
     __shared__ float2 sm[2][32];
     extern __shared__ float4 places[];  // the threads' weights; at the end the warps' column sums
-    Group<L> g;
+    Group<L, WARPS> g;
     const int off = row_offset<T, ALIGNED>(g.row, d);
     const T *x_end = x + n * d, *dy_end = dy + n * d;
     const Weights<TW, CH, ALIGNED> ww(w, places, g.lane, g.size, off, d);
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(L > 0 ? K7_THREADS : 512, L > 0 ? K7_GRAD_BLOC
         // the block's column sums: lane groups that have the same columns, then
         // the rest in order
         constexpr int RPW = 32 / L;
-        constexpr int ROWS = ALIGNED ? K7_WARPS : K7_WARPS * RPW;  // rows of `red`
+        constexpr int ROWS = ALIGNED ? WARPS : WARPS * RPW;  // rows of `red`
         constexpr int WIDTH = L * CH * 8;
         float* red = reinterpret_cast<float*>(places);  // [ROWS][WIDTH], by chunk
         const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / L;
@@ -427,11 +436,12 @@ __global__ void __launch_bounds__(L > 0 ? K7_THREADS : 512, L > 0 ? K7_GRAD_BLOC
                                                (i / 4 * L + g.lane) * 8 + i % 4 * 2) = s;
             }
             __syncthreads();
-            for (int e = threadIdx.x; e < d; e += K7_THREADS) {
+            for (int e = threadIdx.x; e < d; e += 32 * WARPS) {
                 float s = 0.f;
-                // row q of `red` is of rows congruent to q modulo 8
+                // row q of `red` is of rows congruent to the block's first + q modulo 8
+                const int64_t at = (int64_t)blockIdx.x * WARPS * RPW;
 #pragma unroll 8
-                for (int q = 0; q < ROWS; ++q) s += red[q * WIDTH + e + row_offset<T, ALIGNED>(q, d)];
+                for (int q = 0; q < ROWS; ++q) s += red[q * WIDTH + e + row_offset<T, ALIGNED>(at + q, d)];
                 row[which * d + e] = s;
             }
         }
@@ -564,7 +574,9 @@ int row_blocks(int64_t n, int cap) {
 
 int grad_blocks(int64_t n, const RowShape& r, int sm_count) {
     if (r.L == 0) return row_blocks(n, (r.CH == 1 ? 1024 : r.CH == 2 ? 768 : 512) / r.threads * sm_count / 8 * 8);
-    return grid_for(n, K7_WARPS * (32 / r.L), K7_GRAD_BLOCKS * sm_count);
+    if (r.CH < 4) return grid_for(n, grad_warps<1>() * (32 / r.L), grad_resident<1>() * sm_count);
+    // an even number, so that a warp's rows agree modulo 8
+    return grid_for(n, grad_warps<4>(), grad_resident<4>() * (sm_count / 2 * 2));
 }
 
 struct LnArgs {
@@ -583,9 +595,10 @@ cudaError_t ln_launch(const LnArgs& a, bool grad, const RowShape& r) {
     const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.dy);
     const TW *w = static_cast<const TW*>(a.w), *bias = static_cast<const TW*>(a.bias);
     T* y = static_cast<T*>(a.y);
-    const int threads = L > 0 ? K7_THREADS : r.threads;
+    const int warps = grad ? grad_warps<CH>() : K7_WARPS;
+    const int threads = L > 0 ? 32 * warps : r.threads;
     const int own = ALIGNED ? 0 : threads * CH * 32;  // a thread's weights
-    const int red = L > 0 ? (ALIGNED ? K7_WARPS : K7_WARPS * 32 / (L > 0 ? L : 1)) * L * CH * 32 : 0;
+    const int red = L > 0 ? (ALIGNED ? warps : warps * 32 / (L > 0 ? L : 1)) * L * CH * 32 : 0;
     const int smem = grad ? (red > own ? red : own) : 2 * own;
     const void* kernel = grad ? reinterpret_cast<const void*>(&k7_layernorm_grad<T, TW, L, CH, ALIGNED>)
                               : reinterpret_cast<const void*>(&k7_layernorm<T, TW, L, CH, ALIGNED>);

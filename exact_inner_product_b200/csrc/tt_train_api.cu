@@ -13,14 +13,21 @@
 #include "../../include/tt.h"
 #include "tt_internal.h"
 
-#define TT_CUDA(call, what)                                \
-    do {                                                   \
-        const cudaError_t _e = (call);                     \
-        if (_e != cudaSuccess) return cuda_fail(_e, what); \
+#define TT_CUDA(call, what)                                 \
+    do {                                                    \
+        const cudaError_t _e = (call);                      \
+        if (_e != cudaSuccess) return call_failed(_e, what); \
     } while (0)
 
 namespace tt {
 namespace {
+
+// A failed launch or copy: the message is kept, and the runtime's last error
+// cleared, so that a later call does not report this one's.
+tt_status call_failed(cudaError_t e, const char* what) {
+    cudaGetLastError();
+    return cuda_fail(e, what);
+}
 
 size_t elem_bytes(int dtype) { return dtype == TT_F32 ? 4 : 2; }
 
@@ -151,7 +158,7 @@ tt_status clip(const ClipList& l, bool scale, float max_norm, float* norm, void*
     if ((st = check_device_ptr(workspace, "workspace")) != TT_OK) return st;
     const cudaError_t e = launch_clip(l, scale, max_norm, norm, static_cast<double*>(workspace),
                                       static_cast<cudaStream_t>(stream), sms);
-    return e == cudaSuccess ? TT_OK : cuda_fail(e, "gradient norm");
+    return e == cudaSuccess ? TT_OK : call_failed(e, "gradient norm");
 }
 
 tt_status check_embedding(int64_t rows, int32_t d, int32_t id_bytes, int64_t m, float scale) {
@@ -184,7 +191,7 @@ tt_status embedding_grad(const EmbeddingGrad& g, bool by_row, size_t workspace_b
     b.out(g.workspace, need, "workspace");
     if ((st = b.check()) != TT_OK) return st;
     const cudaError_t e = launch_embedding_grad(g, by_row, static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : cuda_fail(e, "embedding gradient");
+    return e == cudaSuccess ? TT_OK : call_failed(e, "embedding gradient");
 }
 
 }  // namespace
@@ -216,7 +223,7 @@ tt_status tt_layernorm(const void* x, tt_dtype dtype, int64_t n, int32_t d, cons
     if ((st = b.check()) != TT_OK) return st;
     const cudaError_t e = launch_layernorm(x, dtype, n, d, w, bias, w_dtype, eps, y, mean, rstd,
                                            static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : cuda_fail(e, "layer norm");
+    return e == cudaSuccess ? TT_OK : call_failed(e, "layer norm");
 }
 
 tt_status tt_layernorm_grad_workspace(int64_t n, int32_t d, size_t* bytes) {
@@ -255,7 +262,7 @@ tt_status tt_layernorm_grad(const void* grad_y, const void* x, tt_dtype dtype, i
     const cudaError_t e =
         launch_layernorm_grad(grad_y, x, dtype, n, d, w, w_dtype, mean, rstd, grad_x, grad_w, grad_bias,
                               static_cast<float*>(workspace), static_cast<cudaStream_t>(stream), sms);
-    return e == cudaSuccess ? TT_OK : cuda_fail(e, "layer norm gradient");
+    return e == cudaSuccess ? TT_OK : call_failed(e, "layer norm gradient");
 }
 
 tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x, tt_dtype dtype, int64_t n, int32_t d,
@@ -275,7 +282,7 @@ tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x,
     if (st != TT_OK) return st;
     const cudaError_t e = launch_normalize_grad(grad_y, g_dtype, x, dtype, n, d, grad_x,
                                                 static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : cuda_fail(e, "normalisation gradient");
+    return e == cudaSuccess ? TT_OK : call_failed(e, "normalisation gradient");
 }
 
 tt_status tt_clip_grad_norm_workspace(int32_t count, const int64_t* n, const int32_t* dtypes, size_t* bytes) {
@@ -314,7 +321,7 @@ tt_status tt_embedding(const void* table, tt_dtype table_dtype, int64_t rows, in
     if ((st = b.check()) != TT_OK) return st;
     const cudaError_t e = launch_embedding(table, table_dtype, rows, d, ids, id_bytes, m, scale, out, out_dtype,
                                            static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : cuda_fail(e, "embedding lookup");
+    return e == cudaSuccess ? TT_OK : call_failed(e, "embedding lookup");
 }
 
 tt_status tt_embedding_grad_workspace(int64_t m, int64_t rows, int32_t d, size_t* bytes) {
@@ -345,7 +352,7 @@ tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64_t m, c
 static tt_status softmax_grad_sizes(int32_t b, int32_t nc, int32_t d, bool with_ids) {
     if (b < 0 || nc < b || d <= 0) return TT_ERR_INVALID_ARG;
     if (d % 16 != 0 || d < 64 || d > TT_MAX_D) return TT_ERR_UNSUPPORTED;
-    if (with_ids && nc > (1 << 28)) return TT_ERR_UNSUPPORTED;
+    if (nc > (with_ids ? 1 << 28 : 1 << 30)) return TT_ERR_UNSUPPORTED;
     return TT_OK;
 }
 
@@ -423,7 +430,7 @@ tt_status tt_inbatch_softmax_grad(const void* users, const void* items, tt_dtype
     g.grad_items = grad_items;
     g.workspace = workspace;
     const cudaError_t e = launch_softmax_grad(pl, g, s, sms);
-    return e == cudaSuccess ? TT_OK : cuda_fail(e, "in-batch softmax gradient");
+    return e == cudaSuccess ? TT_OK : call_failed(e, "in-batch softmax gradient");
 }
 
 }  // extern "C"

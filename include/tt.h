@@ -583,7 +583,7 @@ TT_API tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64
  * needs finite item rows, padding included.)
  *
  * users, items, dtype, b, nc, d, tau, logq, item_ids, valid
- *             as for tt_inbatch_softmax, and the same values
+ *             as for tt_inbatch_softmax, and the same values (nc at most 2^30)
  * lse, loss   device f32 [b]: what tt_inbatch_softmax wrote
  * grad_loss   device f32 [b], the gradient of loss, or NULL for zeros
  * grad_mean   device f32 [1], the gradient of mean, or NULL for zero

@@ -158,6 +158,19 @@ def test_padding_holds_anything():
     assert bool((got[0][bad[:400]] == 0).all()) and bool((got[1][bad] == 0).all())
 
 
+@pytest.mark.parametrize("shift", [1, 4, 8, 16])
+def test_masks_that_begin_anywhere(shift):
+    """valid, logq and item_ids as views into longer tensors, at any element."""
+    _cuda()
+    w = W.batch("inbatch_b8192_d64", b=333, nc=700, d=64, catalogue=300, pad_rate=0.2)
+    inp = W.batch_inputs(w, "cuda")
+    for name in ("valid", "logq", "item_ids"):
+        long = torch.zeros(700 + shift, dtype=inp[name].dtype, device="cuda")
+        long[shift:] = inp[name]
+        inp[name] = long[shift:]
+    _check(inp, w.tau, FULL)
+
+
 def test_edge_batches():
     _cuda()
     d = 64
@@ -279,6 +292,26 @@ def test_side_stream_and_graph():
     lse, loss, _ = tt.tt_inbatch_softmax(inp["users"], inp["items"], w.tau, **args)
     want = tt.tt_inbatch_softmax_grad(inp["users"], inp["items"], lse, loss, w.tau, grad_mean=one, **args)
     assert all(torch.equal(a, b) for a, b in zip(grads, want))
+
+
+def test_memory_made_for_another_stream():
+    """A call on a stream of its own: the workspace it makes is not handed out
+    again on the current stream while its kernels still use it."""
+    _cuda()
+    w = W.batch("inbatch_b8192_d64", b=2000, nc=4000, d=128, catalogue=300)
+    inp = W.batch_inputs(w, "cuda")
+    args = _args(inp, FULL)
+    one = torch.ones((), device="cuda")
+    lse, loss, _ = tt.tt_inbatch_softmax(inp["users"], inp["items"], w.tau, **args)
+    want = tt.tt_inbatch_softmax_grad(inp["users"], inp["items"], lse, loss, w.tau, grad_mean=one, **args)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    need = tt.tt_inbatch_softmax_grad_workspace(2000, 4000, 128, True, True)
+    for _ in range(10):
+        got = tt.tt_inbatch_softmax_grad(inp["users"], inp["items"], lse, loss, w.tau, grad_mean=one, stream=side, **args)
+        torch.empty(need, dtype=torch.uint8, device="cuda").fill_(255)  # on the current stream, at once
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_refusals():
