@@ -28,13 +28,22 @@
 //   k6_finish    adds the partial products of each row, the diagonal, and the
 //                scale, and rounds to bf16
 //
-// P is rounded to bf16 (a relative 2^-9 of each term, of either sign): its
-// products with bf16 rows are then exact and add in fp32, and what the
+// P is rounded to bf16 (at most a relative 2^-8 of each term, of either sign):
+// its products with bf16 rows are then exact and add in fp32, and what the
 // rounding leaves is of the size of the result's own rounding to bf16.
 // Recomputing the logits in both passes costs 2 of the 8 b nc d operations and
 // a second exponential per logit; one pass would need either atomic additions
 // of b x d (or nc x d) sums per tile, whose order changes the result, or
-// their partial sums in HBM.
+// their partial sums in HBM (2.1 GB at 16384 x 32768 x 128).
+//
+// Bound by the tensor cores for d >= 128 and by the exponentials below; the
+// epilogue (about 4 instructions per logit, 2 more with item ids) overlaps with
+// both by two groups of warps and two to three logit tiles in flight. Measured
+// on a B200, 8 b nc d operations in k6_products: 16384 x 32768 x 128 412 us
+// (1.33 PFLOP/s) without masks, 460 us with all; 16384^2 x 256 429 us (1.28);
+// 32768^2 x 64 without masks 686 us (3.1 T exponentials/s); 8192^2 x 512 687 us
+// (one stage of rows fits beside the kept tile, and the logits are formed for
+// each half of the columns).
 //
 // The tiles of both passes, row tile after row tile, form one line that is cut
 // evenly among the SMs, so a few row tiles with long sums use the whole GPU
@@ -57,7 +66,12 @@ namespace tt {
 namespace {
 
 constexpr int K6_M = 128;            // kept rows per tile (TMEM lanes)
-constexpr int K6_GROUPS = 2;         // groups of four epilogue warps, one tile each in turn
+// Groups of four epilogue warps, one tile each in turn. At most as many as there
+// are logit buffers (2 at least): a group that waits for a tile has seen the
+// logits of the tile K6_GROUPS before it, and with it every earlier round of the
+// buffer, so the parity it waits for cannot be that of a round before.
+constexpr int K6_GROUPS = 2;
+static_assert(K6_GROUPS <= 2, "no more than the fewest logit buffers");
 constexpr int K6_EPI_WARPS = 4 * K6_GROUPS;
 constexpr int K6_THREADS = 32 * (4 + K6_EPI_WARPS);  // warps 0-3: copies, logits, products, none
 // Registers: the four first warps give back what the epilogue takes.
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
 #pragma unroll 1
                 for (int h = 0; h < TN / 64; ++h) {
                     f32x2 cb[8];
-                    int2 cg[8];
+                    [[maybe_unused]] int2 cg[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         cb[e] = *reinterpret_cast<const f32x2*>(cs + h * 64 + 8 * e + col0);
@@ -704,11 +718,14 @@ int stages_for(int kchunks) {
 SoftmaxGradPlan softmax_grad_plan(int b, int nc, int d, bool item_ids, bool copies, int sm_count) {
     SoftmaxGradPlan pl;
     const int kchunks = (d + 63) / 64;
-    pl.tile_cols = d <= 128 ? 128 : 64;
+    // 64 columns where shared memory holds no two tiles of 128 rows of 5 pieces and
+    // more (the logits' products read the kept tile twice as often then: 16384^2 x
+    // 256 436 against 429 us)
+    pl.tile_cols = d <= 256 ? 128 : 64;
     pl.halves = (d + K6_HALF - 1) / K6_HALF;
     pl.width = d < K6_HALF ? d : K6_HALF;
     const int acc = (pl.width + 31) / 32 * 32;
-    pl.bufs = (K6_TMEM_COLS - acc) / pl.tile_cols;
+    pl.bufs = (K6_TMEM_COLS - acc) / pl.tile_cols;  // 2 to 4
     if (pl.bufs > K6_MAX_BUFS) pl.bufs = K6_MAX_BUFS;
     pl.stages = pl.tile_cols == 128 ? stages_for<128>(kchunks) : stages_for<64>(kchunks);
     int64_t units;
