@@ -658,63 +658,76 @@ def tt_embedding_grad_rows(ids: torch.Tensor, grad: torch.Tensor, rows: int, sca
 _ELEM = {torch.float32: TT_F32, torch.bfloat16: TT_BF16}
 
 
-def _tensor_list(name: str, tensors, like=None):
-    """Addresses of contiguous float32/bfloat16 CUDA tensors, as an array of 64-bit integers."""
-    good = all([t.is_cuda and t.is_contiguous() and t.dtype in _ELEM for t in tensors])
-    if good and like is not None:
-        good = all([t.dtype == o.dtype and t.shape == o.shape for t, o in zip(tensors, like)])
-    if not good:  # say which
-        for i, t in enumerate(tensors):
-            if t.dtype not in _ELEM:
-                raise TypeError(f"{name}[{i}] must be float32 or bfloat16, got {t.dtype}")
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor")
-            if like is not None and (t.dtype != like[i].dtype or t.shape != like[i].shape):
-                raise ValueError(f"{name}[{i}] must have the dtype and shape of its gradient")
-    return array.array("Q", [t.data_ptr() for t in tensors])
+_NUMEL, _DATA_PTR, _CONTIGUOUS = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.is_contiguous
+
+
+def _tensor_list(tensors):
+    """Addresses, element counts and dtype codes of contiguous tensors, as arrays of 64-, 64- and 32-bit integers
+    (few passes over the list: its length sets the call's time). None if one is not float32 or bfloat16, or not
+    contiguous."""
+    try:
+        codes = array.array("i", [_ELEM[t.dtype] for t in tensors])
+    except KeyError:
+        return None
+    if not all(map(_CONTIGUOUS, tensors)):
+        return None
+    return array.array("Q", list(map(_DATA_PTR, tensors))), array.array("q", list(map(_NUMEL, tensors))), codes
+
+
+def _explain_list(name: str, tensors, like=None) -> None:
+    """Raise for the tensor that a list call cannot take."""
+    for i, t in enumerate(tensors):
+        if t.dtype not in _ELEM:
+            raise TypeError(f"{name}[{i}] must be float32 or bfloat16, got {t.dtype}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be a contiguous CUDA tensor")
+        if like is not None and (t.dtype != like[i].dtype or t.numel() != like[i].numel()):
+            raise ValueError(f"{name}[{i}] must have the dtype and size of its gradient")
+
+
+def _address(a) -> int:
+    return a.buffer_info()[0]
+
+
+def _clip_workspace(lists) -> int:
+    need = ctypes.c_size_t(0)
+    _check(_lib.tt_clip_grad_norm_workspace(len(lists[0]), _address(lists[1]), _address(lists[2]), ctypes.byref(need)),
+           "tt_clip_grad_norm_workspace")
+    return int(need.value)
 
 
 def _norm_call(tensors, norm, workspace, stream):
     tensors = list(tensors)
-    count = len(tensors)
-    ptrs = _tensor_list("grads", tensors)
-    n = array.array("q", [t.numel() for t in tensors])
-    dtypes = array.array("i", [_ELEM[t.dtype] for t in tensors])
-    n_at, dtypes_at = n.buffer_info()[0], dtypes.buffer_info()[0]
-    dev = tensors[0].device if count else torch.device("cuda", torch.cuda.current_device())
+    lists = _tensor_list(tensors)
+    dev = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+    if lists is None or dev.type != "cuda":
+        _explain_list("grads", tensors)
     if norm is None:
         with _on(stream):
             norm = torch.empty((), dtype=torch.float32, device=dev)
     else:
         _check_float("norm", norm, (), (torch.float32,), dev)
-    if workspace is None:
-        need = ctypes.c_size_t(0)
-        _check(_lib.tt_clip_grad_norm_workspace(count, n_at, dtypes_at, ctypes.byref(need)), "tt_clip_grad_norm_workspace")
-        with _on(stream):
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=dev)
-    else:
-        _check_float("workspace", workspace, dtypes=(torch.uint8,), device=dev)
-    # the arrays come along: their addresses are used
-    return tensors, count, ptrs, (n, n_at), (dtypes, dtypes_at), norm, workspace
+    return tensors, lists, norm, _workspace(workspace, _clip_workspace(lists) if workspace is None else 0, dev, stream)
 
 
 def tt_clip_grad_norm_workspace(grads) -> int:
     """Bytes of device workspace ``tt_grad_norm`` and ``tt_clip_grad_norm`` need for these tensors."""
     grads = list(grads)
-    need = ctypes.c_size_t(0)
-    n = array.array("q", [t.numel() for t in grads])
-    dtypes = array.array("i", [_dtype(t) for t in grads])
-    _check(_lib.tt_clip_grad_norm_workspace(len(grads), n.buffer_info()[0], dtypes.buffer_info()[0], ctypes.byref(need)),
-           "tt_clip_grad_norm_workspace")
-    return int(need.value)
+    lists = _tensor_list(grads)
+    if lists is None:
+        _explain_list("grads", grads)
+    return _clip_workspace(lists)
 
 
 def tt_grad_norm(grads, norm: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """The L2 norm of all elements of the tensors ``grads`` (float32 and
     bfloat16 may be mixed), as a float32 scalar on the device (``tt_grad_norm``)."""
-    _, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace, stream)
-    _check(_lib.tt_grad_norm(count, ptrs.buffer_info()[0], n[1], dtypes[1], _ptr(norm), _ptr(workspace), workspace.numel(), _stream(stream)),
-           "tt_grad_norm")
+    grads, (ptrs, n, codes), norm, workspace = _norm_call(grads, norm, workspace, stream)
+    status = _lib.tt_grad_norm(len(grads), _address(ptrs), _address(n), _address(codes), _ptr(norm), _ptr(workspace),
+                               workspace.numel(), _stream(stream))
+    if status != TT_OK:
+        _explain_list("grads", grads)
+        _check(status, "tt_grad_norm")
     return norm
 
 
@@ -722,18 +735,25 @@ def tt_clip_grad_norm(grads, max_norm: float, out=None, norm: torch.Tensor | Non
                       workspace: torch.Tensor | None = None, stream=None):
     """Scale the tensors ``grads`` so that their global L2 norm is at most
     ``max_norm`` (``tt_clip_grad_norm``): in place, or into the tensors of
-    ``out``. Returns the norm before the scaling, a float32 scalar on the
-    device; nothing is read back to the host."""
-    grads, count, ptrs, n, dtypes, norm, workspace = _norm_call(grads, norm, workspace, stream)
+    ``out`` (same dtypes and sizes). Returns the norm before the scaling, a
+    float32 scalar on the device; nothing is read back to the host."""
+    grads, (ptrs, n, codes), norm, workspace = _norm_call(grads, norm, workspace, stream)
     outs = None
     if out is not None:
         out = list(out)
-        if len(out) != count:
-            raise ValueError(f"out has {len(out)} tensors for {count} gradients")
-        outs = _tensor_list("out", out, like=grads)
-    _check(_lib.tt_clip_grad_norm(count, ptrs.buffer_info()[0], n[1], dtypes[1],
-                                  None if outs is None else outs.buffer_info()[0], float(max_norm), _ptr(norm), _ptr(workspace),
-                                  workspace.numel(), _stream(stream)), "tt_clip_grad_norm")
+        if len(out) != len(grads):
+            raise ValueError(f"out has {len(out)} tensors for {len(grads)} gradients")
+        outs = _tensor_list(out)
+        if outs is None or outs[1] != n or outs[2] != codes:
+            _explain_list("out", out, grads)
+    status = _lib.tt_clip_grad_norm(len(grads), _address(ptrs), _address(n), _address(codes),
+                                    None if outs is None else _address(outs[0]), float(max_norm), _ptr(norm),
+                                    _ptr(workspace), workspace.numel(), _stream(stream))
+    if status != TT_OK:
+        _explain_list("grads", grads)
+        if out is not None:
+            _explain_list("out", out)
+        _check(status, "tt_clip_grad_norm")
     return norm
 
 

@@ -37,6 +37,38 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
     return x < y + b_bytes && y < x + a_bytes;
 }
 
+// Device pointers of a call, one query per allocation: what lies in the
+// allocation of the pointer checked last needs none (a list of a few hundred
+// gradients is mostly views into few of them).
+class DeviceCheck {
+    uintptr_t lo = 0, hi = 0;
+    typedef CUresult (*RangeFn)(CUdeviceptr*, size_t*, CUdeviceptr);
+    static RangeFn range_fn() {
+        static const RangeFn fn = [] {
+            void* p = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            const cudaError_t e = cudaGetDriverEntryPoint("cuMemGetAddressRange", &p, cudaEnableDefault, &q);
+            return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<RangeFn>(p) : nullptr;
+        }();
+        return fn;
+    }
+
+public:
+    tt_status operator()(const void* p, const char* name) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        if (p == nullptr || (at >= lo && at < hi)) return TT_OK;
+        const tt_status st = check_device_ptr(p, name);
+        if (st != TT_OK) return st;
+        CUdeviceptr base = 0;
+        size_t size = 0;
+        if (range_fn() != nullptr && range_fn()(&base, &size, (CUdeviceptr)at) == CUDA_SUCCESS) {
+            lo = (uintptr_t)base;
+            hi = lo + size;
+        }
+        return TT_OK;
+    }
+};
+
 // The buffers of a call. Outputs may overlap nothing; inputs may overlap
 // inputs. Null buffers are skipped.
 struct Buffers {
@@ -63,8 +95,9 @@ struct Buffers {
                     set_last_error_message(msg);
                     return TT_ERR_INVALID_ARG;
                 }
+        DeviceCheck device;
         for (int i = 0; i < count; ++i) {
-            const tt_status st = check_device_ptr(list[i].p, list[i].name);
+            const tt_status st = device(list[i].p, list[i].name);
             if (st != TT_OK) return st;
         }
         return TT_OK;
@@ -142,6 +175,7 @@ tt_status clip(const ClipList& l, bool scale, float max_norm, float* norm, void*
     const size_t need = clip_workspace_bytes(l, sms);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != TT_OK) return st;
     if (scale && (st = check_clip_overlap(l)) != TT_OK) return st;
+    DeviceCheck grads, outs;
     for (int i = 0; i < l.count; ++i) {
         if (l.n[i] == 0) continue;
         const size_t bytes = (size_t)l.n[i] * elem_bytes(l.dtype[i]);
@@ -150,8 +184,8 @@ tt_status clip(const ClipList& l, bool scale, float max_norm, float* norm, void*
             set_last_error_message("norm or workspace overlaps a tensor");
             return TT_ERR_INVALID_ARG;
         }
-        if ((st = check_device_ptr(l.in[i], "grads")) != TT_OK) return st;
-        if (scale && l.out[i] != l.in[i] && (st = check_device_ptr(l.out[i], "out")) != TT_OK) return st;
+        if ((st = grads(l.in[i], "grads")) != TT_OK) return st;
+        if (scale && l.out[i] != l.in[i] && (st = outs(l.out[i], "out")) != TT_OK) return st;
     }
     if (overlap(norm, 4, workspace, need)) return TT_ERR_INVALID_ARG;
     if ((st = check_device_ptr(norm, "norm")) != TT_OK) return st;
