@@ -606,10 +606,13 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
     const int n = *a.cross_count;
     const int e = (blockIdx.y * 32 + lane) * E;
     const bool in = e < a.d;
-    for (int b = blockIdx.x * K8_JOIN_WARPS; b < n; b += gridDim.x * K8_JOIN_WARPS) {
+    // Neighbours in the list go to different blocks: the longest runs, of the
+    // lowest ids where those are the popular ones, stand side by side.
+    const int grid = gridDim.x;
+    for (int b = blockIdx.x; b < n; b += grid * K8_JOIN_WARPS) {
         int64_t k = 0;  // blocks after the first that the run reaches
-        if (b + warp < n) {
-            const int64_t c = a.cross[b + warp].x;
+        if (b + warp * grid < n) {
+            const int64_t c = a.cross[b + warp * grid].x;
             const uint32_t key = a.key(c * K8_BLOCK + K8_BLOCK - 1);
             while (true) {
                 const int64_t i = (c + 1 + k + lane) * K8_BLOCK;
@@ -622,7 +625,7 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
         if (lane == 0) reach[warp] = k;
         __syncthreads();
         if (k > 0 && k <= K8_JOIN_WARP && in) {
-            const int2 run = a.cross[b + warp];
+            const int2 run = a.cross[b + warp * grid];
             float acc[E];
             Raw<float, E> r;
             r.load(a.part + ((int64_t)run.x * 2 + 1) * a.d + e);
@@ -635,7 +638,7 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
         for (int w = 0; w < K8_JOIN_WARPS; ++w) {
             const int64_t kw = reach[w];
             if (kw <= K8_JOIN_WARP) continue;  // the same for the whole block
-            const int2 run = a.cross[b + w];
+            const int2 run = a.cross[b + w * grid];
             float acc[E];
 #pragma unroll
             for (int j = 0; j < E; ++j) acc[j] = 0.f;
