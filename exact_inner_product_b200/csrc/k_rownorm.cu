@@ -28,7 +28,7 @@
 // thread's columns, stay the same from row to row: the column sums stay in
 // registers, and the thread's weights, loaded once, in its own shared memory
 // (element by element, 100000 x 777 bf16 took 432 us forward and 602 us back; so
-// 169 and 256).
+// 128 and 161, beside 86 and 115 for 776).
 //
 // The column sums dw and dbias: each thread keeps its columns' sums in
 // registers over all the rows it handles, the block adds its warps' sums in
@@ -89,51 +89,64 @@ __device__ __forceinline__ void store_pairs8(T* p, const f32x2* v) {
     store_row<8>(p, x);
 }
 
-// The columns of a chunk that belong to the row: elements lo .. hi - 1 of 8.
-struct Cut {
-    int lo, hi;
-    __device__ __forceinline__ Cut(int col, int d) : lo(col < 0 ? -col : 0), hi(d - col < 8 ? d - col : 8) {}
-    __device__ __forceinline__ bool whole() const { return lo == 0 && hi == 8; }
-};
+// Which of the 8 elements of the chunk at column col belong to the row, as bits.
+constexpr uint32_t WHOLE = 0xFFu;
+__device__ __forceinline__ uint32_t kept(int col, int d) {
+    const int lo = col < 0 ? -col : 0, hi = d - col < 8 ? d - col : 8;
+    return lo < hi ? (WHOLE >> (8 - hi)) & (WHOLE << lo) : 0u;
+}
+// x where bit k is set, else 0.
+__device__ __forceinline__ float keep_f32(float x, uint32_t keep, int k) { return keep >> k & 1u ? x : 0.f; }
+// The chunk with zeros where it is not kept.
+__device__ __forceinline__ void clear_others(Raw<__nv_bfloat16, 8>& r, uint32_t keep) {
+    if (keep == WHOLE) return;
+    auto mask = [&](int j) {
+        return (keep >> (2 * j) & 1u ? 0xFFFFu : 0u) | (keep >> (2 * j + 1) & 1u ? 0xFFFF0000u : 0u);
+    };
+    r.a.x &= mask(0), r.a.y &= mask(1), r.a.z &= mask(2), r.a.w &= mask(3);
+}
+__device__ __forceinline__ void clear_others(Raw<float, 8>& r, uint32_t keep) {
+    if (keep == WHOLE) return;
+    r.a = make_float4(keep_f32(r.a.x, keep, 0), keep_f32(r.a.y, keep, 1), keep_f32(r.a.z, keep, 2),
+                      keep_f32(r.a.w, keep, 3));
+    r.b = make_float4(keep_f32(r.b.x, keep, 4), keep_f32(r.b.y, keep, 5), keep_f32(r.b.z, keep, 6),
+                      keep_f32(r.b.w, keep, 7));
+}
 
-// The chunk of memory at p (16-byte aligned), zeros outside the cut; `end` is the
-// tensor's, past which nothing is read.
-__device__ __forceinline__ void load_cut(Raw<__nv_bfloat16, 8>& r, const __nv_bfloat16* p, const Cut& c,
-                                         const __nv_bfloat16* end) {
-    const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
-    auto in = [&](int k) { return k >= c.lo && k < c.hi; };
+// The chunk of memory at p (16-byte aligned); `end` is the tensor's, past which
+// nothing is read (zeros). What is not the row's is cleared where the chunk is
+// used: done here it would wait for the load.
+__device__ __forceinline__ void load_chunk(Raw<__nv_bfloat16, 8>& r, const __nv_bfloat16* p, const __nv_bfloat16* end) {
     if (p + 8 <= end) {
         r.load(p);
-        if (c.whole()) return;
-        auto mask = [&](int j) { return (in(2 * j) ? 0xFFFFu : 0u) | (in(2 * j + 1) ? 0xFFFF0000u : 0u); };
-        r.a.x &= mask(0), r.a.y &= mask(1), r.a.z &= mask(2), r.a.w &= mask(3);
     } else {
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
         auto word = [&](int j) {
-            return (in(2 * j) ? (uint32_t)u[2 * j] : 0u) | (in(2 * j + 1) ? (uint32_t)u[2 * j + 1] << 16 : 0u);
+            return (p + 2 * j < end ? (uint32_t)u[2 * j] : 0u) | (p + 2 * j + 1 < end ? (uint32_t)u[2 * j + 1] << 16 : 0u);
         };
         r.a = make_uint4(word(0), word(1), word(2), word(3));
     }
 }
-__device__ __forceinline__ void load_cut(Raw<float, 8>& r, const float* p, const Cut& c, const float* end) {
-    if (p + 8 <= end && c.whole()) {
+__device__ __forceinline__ void load_chunk(Raw<float, 8>& r, const float* p, const float* end) {
+    if (p + 8 <= end) {
         r.load(p);
-        return;
+    } else {
+        auto one = [&](int k) { return p + k < end ? __ldg(p + k) : 0.f; };
+        r.a = make_float4(one(0), one(1), one(2), one(3));
+        r.b = make_float4(one(4), one(5), one(6), one(7));
     }
-    auto one = [&](int k) { return k >= c.lo && k < c.hi ? __ldg(p + k) : 0.f; };
-    r.a = make_float4(one(0), one(1), one(2), one(3));
-    r.b = make_float4(one(4), one(5), one(6), one(7));
 }
 template <typename T>
-__device__ __forceinline__ void store_cut(T* p, const f32x2* v, const Cut& c) {
-    if (c.whole()) {
+__device__ __forceinline__ void store_kept(T* p, const f32x2* v, uint32_t keep) {
+    if (keep == WHOLE) {
         store_pairs8(p, v);
         return;
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const float2 u = unpair(v[k]);
-        if (2 * k >= c.lo && 2 * k < c.hi) store_row<1>(p + 2 * k, &u.x);
-        if (2 * k + 1 >= c.lo && 2 * k + 1 < c.hi) store_row<1>(p + 2 * k + 1, &u.y);
+        if (keep >> (2 * k) & 1u) store_row<1>(p + 2 * k, &u.x);
+        if (keep >> (2 * k + 1) & 1u) store_row<1>(p + 2 * k + 1, &u.y);
     }
 }
 
@@ -232,12 +245,24 @@ __device__ __forceinline__ int row_offset(int64_t row, int d) {
     return (int)(row * d % (16 / (int)sizeof(T)));
 }
 
+// Rows a group has at hand at once: narrow rows are short loads, and several of
+// them share the weights and hide each other's sums (400000 x 200 bf16: 120 to
+// 114 us forward, 142 to 126 back; 10^6 x 40 fp32 113 to 93 back).
+template <int L, int CH, bool ALIGNED>
+constexpr int forward_rows() { return ALIGNED && L > 0 && CH == 1 ? 2 : 1; }
+template <int CH>
+constexpr int grad_rows() { return CH == 1 ? 4 : 2; }
+
 template <typename T, typename TW, int L, int CH, bool ALIGNED>
 __global__ void __launch_bounds__(L > 0 ? K7_THREADS : 512)
     k7_layernorm(const T* __restrict__ x, const TW* __restrict__ w, const TW* __restrict__ bias, T* __restrict__ y,
                  float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t n, int d, float eps) {
-    // a warp per row: the other warps' loads do as well (148 against 158 us at 200003 x 512)
-    constexpr bool AHEAD = L == 0;
+    constexpr int R = forward_rows<L, CH, ALIGNED>();
+    // The next row's loads ahead pay where a block has a row, and for rows whose
+    // first and last chunks need work before the sums (400000 x 201 bf16 177 against
+    // 144 us); with a warp per whole row the other warps' loads do as well (200003 x
+    // 512 bf16: 158 us ahead, 148 not), and so they do with four chunks.
+    constexpr bool AHEAD = L == 0 ? ALIGNED : !ALIGNED && CH <= 2;
     __shared__ float2 sm[2][32];
     extern __shared__ float4 places[];
     Group<L> g;
@@ -245,74 +270,138 @@ __global__ void __launch_bounds__(L > 0 ? K7_THREADS : 512)
     const T* end = x + n * d;
     const Weights<TW, CH, ALIGNED> ww(w, places, g.lane, g.size, off, d);
     const Weights<TW, CH, ALIGNED> bb(bias, places + 2 * CH * blockDim.x, g.lane, g.size, off, d);
-    Raw<T, 8> next[CH];
+    auto column = [&](int c) { return (c * g.size + g.lane) * 8 - off; };
+    uint32_t keep[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) keep[c] = kept(column(c), d);
+    Raw<T, 8> next[R][CH];
     auto load = [&](int64_t row) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int col = (c * g.size + g.lane) * 8 - off;
-            next[c].zero();
-            if (row < n && col < d) {
-                if constexpr (ALIGNED) next[c].load(x + row * d + col);
-                else load_cut(next[c], x + row * d + col, Cut(col, d), end);
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = row + r * g.step;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                next[r][c].zero();
+                if (at < n && keep[c] != 0) {
+                    if constexpr (ALIGNED) next[r][c].load(x + at * d + column(c));
+                    else load_chunk(next[r][c], x + at * d + column(c), end);
+                }
             }
         }
     };
     if (AHEAD) load(g.row);
-    for (; g.any(n); g.row += g.step) {
+    for (; g.any(n); g.row += R * g.step) {
         if (!AHEAD) load(g.row);
-        f32x2 v[CH * 4];
-        f32x2 s = pair(0.f, 0.f);
+        f32x2 v[R][CH * 4];
+        float mean[R], rstd[R];
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            pairs8(next[c], v + 4 * c);
+        for (int r = 0; r < R; ++r) {
+            f32x2 s = pair(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s = add2(s, v[4 * c + k]);
+            for (int c = 0; c < CH; ++c) {
+                if (!ALIGNED) clear_others(next[r][c], keep[c]);
+                pairs8(next[r][c], v[r] + 4 * c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s = add2(s, v[r][4 * c + k]);
+            }
+            mean[r] = sum2(s);
         }
-        const bool live = g.row < n;
-        if (AHEAD) load(g.row + g.step);
-        const float mean = g.sums(sum2(s), 0.f, sm).x / (float)d;
-        const f32x2 minus = pair(-mean, -mean);
-        s = pair(0.f, 0.f);
+        if (AHEAD) load(g.row + R * g.step);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int col = (c * g.size + g.lane) * 8 - off;
-            const Cut cut(col, d);
+        for (int r = 0; r < R; ++r) mean[r] = g.sums(mean[r], 0.f, sm).x / (float)d;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[4 * c + k] = add2(v[4 * c + k], minus);
-                if (ALIGNED || cut.whole()) {
-                    if (col < d) s = fma2(v[4 * c + k], v[4 * c + k], s);
+        for (int r = 0; r < R; ++r) {
+            const f32x2 minus = pair(-mean[r], -mean[r]);
+            f32x2 s = pair(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[r][4 * c + k] = add2(v[r][4 * c + k], minus);
+                if (ALIGNED || keep[c] == WHOLE) {
+                    if (keep[c] != 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) s = fma2(v[r][4 * c + k], v[r][4 * c + k], s);
+                    }
                 } else {
-                    const float2 u = unpair(v[4 * c + k]);
-                    const f32x2 in = pair(2 * k >= cut.lo && 2 * k < cut.hi ? u.x : 0.f,
-                                          2 * k + 1 >= cut.lo && 2 * k + 1 < cut.hi ? u.y : 0.f);
-                    s = fma2(in, in, s);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 u = unpair(v[r][4 * c + k]);
+                        const f32x2 in = pair(keep_f32(u.x, keep[c], 2 * k), keep_f32(u.y, keep[c], 2 * k + 1));
+                        s = fma2(in, in, s);
+                    }
                 }
             }
+            rstd[r] = sum2(s);
         }
-        const float rstd = 1.0f / sqrtf(g.sums(sum2(s), 0.f, sm).x / (float)d + eps);
-        if (!live) continue;
-        const f32x2 r2 = pair(rstd, rstd);
-        T* yr = y + g.row * d;
+#pragma unroll
+        for (int r = 0; r < R; ++r) rstd[r] = 1.0f / sqrtf(g.sums(rstd[r], 0.f, sm).x / (float)d + eps);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int col = (c * g.size + g.lane) * 8 - off;
-            if (col >= d) continue;
-            f32x2 out[4], wv[4], bv[4];
-            if (w) ww.get(c, col, wv);
-            if (bias) bb.get(c, col, bv);
+            if (keep[c] == 0) continue;
+            f32x2 wv[4], bv[4];
+            if (w) ww.get(c, column(c), wv);
+            if (bias) bb.get(c, column(c), bv);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                out[k] = mul2(v[4 * c + k], r2);
-                if (w) out[k] = mul2(out[k], wv[k]);
-                if (bias) out[k] = add2(out[k], bv[k]);
+            for (int r = 0; r < R; ++r) {
+                const int64_t at = g.row + r * g.step;
+                if (at >= n) continue;
+                const f32x2 r2 = pair(rstd[r], rstd[r]);
+                f32x2 out[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    out[k] = mul2(v[r][4 * c + k], r2);
+                    if (w) out[k] = mul2(out[k], wv[k]);
+                    if (bias) out[k] = add2(out[k], bv[k]);
+                }
+                if constexpr (ALIGNED) store_pairs8(y + at * d + column(c), out);
+                else store_kept(y + at * d + column(c), out, keep[c]);
             }
-            if constexpr (ALIGNED) store_pairs8(yr + col, out);
-            else store_cut(yr + col, out, Cut(col, d));
         }
-        if (g.lane == 0) {
-            if (mean_out) mean_out[g.row] = mean;
-            if (rstd_out) rstd_out[g.row] = rstd;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = g.row + r * g.step;
+            if (g.lane == 0 && at < n) {
+                if (mean_out) mean_out[at] = mean[r];
+                if (rstd_out) rstd_out[at] = rstd[r];
+            }
+        }
+    }
+}
+
+// The block's column sums to its partial row: lane groups that have the same
+// columns, then the rest in order.
+template <typename T, int L, int CH, int WARPS, bool ALIGNED>
+__device__ __forceinline__ void write_columns(const f32x2* dw, const f32x2* db, const Group<L, WARPS>& g, float* red,
+                                              float* row, int d) {
+    constexpr int RPW = 32 / L;
+    constexpr int ROWS = ALIGNED ? WARPS : WARPS * RPW;  // rows of `red`
+    constexpr int WIDTH = L * CH * 8;                    // [ROWS][WIDTH], by chunk
+    const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / L;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < CH * 4; ++i) {
+            float2 s = unpair(which == 0 ? dw[i] : db[i]);
+            if constexpr (ALIGNED) {
+#pragma unroll
+                for (int o = L; o < 32; o <<= 1) {
+                    s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+                    s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+                }
+            }
+            if (!ALIGNED || sub == 0)
+                *reinterpret_cast<float2*>(red + (ALIGNED ? warp : warp * RPW + sub) * WIDTH +
+                                           (i / 4 * L + g.lane) * 8 + i % 4 * 2) = s;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < d; e += 32 * WARPS) {
+            float s = 0.f;
+            // row q of `red` is of rows congruent to the block's first + q modulo 8
+            const int64_t at = (int64_t)blockIdx.x * WARPS * RPW;
+#pragma unroll 8
+            for (int q = 0; q < ROWS; ++q) s += red[q * WIDTH + e + row_offset<T, ALIGNED>(at + q, d)];
+            row[which * d + e] = s;
         }
     }
 }
@@ -322,7 +411,10 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
     k7_layernorm_grad(const T* __restrict__ dy, const T* __restrict__ x, const TW* __restrict__ w,
                       const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* __restrict__ dx,
                       float* __restrict__ part, int64_t n, int d) {
-    constexpr bool AHEAD = L > 0 || CH <= 2;
+    // The next row's loads ahead, where the registers hold them: fp32 rows of four
+    // chunks do not fit beside the sums (100000 x 776 fp32 314 against 182 us), nor
+    // do unaligned bf16 ones (100000 x 777: 184 against 161 us).
+    constexpr bool AHEAD = CH <= 2 || (L > 0 && ALIGNED && sizeof(T) == 2);
     constexpr int WARPS = grad_warps<CH>();
     __shared__ float2 sm[2][32];
     extern __shared__ float4 places[];  // the threads' weights; at the end the warps' column sums
@@ -348,8 +440,8 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
                     nx[c].load(x + row * d + col);
                     ng[c].load(dy + row * d + col);
                 } else {
-                    load_cut(nx[c], x + row * d + col, Cut(col, d), x_end);
-                    load_cut(ng[c], dy + row * d + col, Cut(col, d), dy_end);
+                    load_chunk(nx[c], x + row * d + col, x_end);
+                    load_chunk(ng[c], dy + row * d + col, dy_end);
                 }
             }
         }
@@ -364,6 +456,11 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
         for (int c = 0; c < CH; ++c) {
             rx[c] = nx[c];
             rg[c] = ng[c];
+            if (!ALIGNED) {
+                const uint32_t keep = kept((c * g.size + g.lane) * 8 - off, d);
+                clear_others(rx[c], keep);
+                clear_others(rg[c], keep);
+            }
         }
         const f32x2 minus = pair(-n_mean, -n_mean), r2 = pair(n_rstd, n_rstd);
         const bool live = g.row < n;
@@ -405,46 +502,13 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
                 out[k] = mul2(fma2(xh, m2, add2(gv[k], m1)), r2);
             }
             if constexpr (ALIGNED) store_pairs8(dx + g.row * d + col, out);
-            else store_cut(dx + g.row * d + col, out, Cut(col, d));
+            else store_kept(dx + g.row * d + col, out, kept(col, d));
         }
     }
     if (part == nullptr) return;
     float* row = part + (int64_t)blockIdx.x * 2 * d;
     if constexpr (L > 0) {
-        // the block's column sums: lane groups that have the same columns, then
-        // the rest in order
-        constexpr int RPW = 32 / L;
-        constexpr int ROWS = ALIGNED ? WARPS : WARPS * RPW;  // rows of `red`
-        constexpr int WIDTH = L * CH * 8;
-        float* red = reinterpret_cast<float*>(places);  // [ROWS][WIDTH], by chunk
-        const int warp = threadIdx.x >> 5, sub = (threadIdx.x & 31) / L;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < CH * 4; ++i) {
-                float2 s = unpair(which == 0 ? dw[i] : db[i]);
-                if constexpr (ALIGNED) {
-#pragma unroll
-                    for (int o = L; o < 32; o <<= 1) {
-                        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-                        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-                    }
-                }
-                if (!ALIGNED || sub == 0)
-                    *reinterpret_cast<float2*>(red + (ALIGNED ? warp : warp * RPW + sub) * WIDTH +
-                                               (i / 4 * L + g.lane) * 8 + i % 4 * 2) = s;
-            }
-            __syncthreads();
-            for (int e = threadIdx.x; e < d; e += 32 * WARPS) {
-                float s = 0.f;
-                // row q of `red` is of rows congruent to the block's first + q modulo 8
-                const int64_t at = (int64_t)blockIdx.x * WARPS * RPW;
-#pragma unroll 8
-                for (int q = 0; q < ROWS; ++q) s += red[q * WIDTH + e + row_offset<T, ALIGNED>(at + q, d)];
-                row[which * d + e] = s;
-            }
-        }
+        write_columns<T, L, CH, WARPS, ALIGNED>(dw, db, g, reinterpret_cast<float*>(places), row, d);
     } else {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -458,6 +522,95 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
             }
         }
     }
+}
+
+// The same for narrow rows (a multiple of 8, up to 512 columns), several at once.
+template <typename T, typename TW, int L, int CH>
+__global__ void __launch_bounds__(K7_THREADS, 2)
+    k7_layernorm_grad_rows(const T* __restrict__ dy, const T* __restrict__ x, const TW* __restrict__ w,
+                           const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* __restrict__ dx,
+                           float* __restrict__ part, int64_t n, int d) {
+    constexpr int R = grad_rows<CH>();
+    extern __shared__ float red[];
+    Group<L> g;
+    auto column = [&](int c) { return (c * L + g.lane) * 8; };
+    f32x2 dw[CH * 4], db[CH * 4];
+#pragma unroll
+    for (int i = 0; i < CH * 4; ++i) dw[i] = db[i] = pair(0.f, 0.f);
+    const float inv_d = 1.0f / (float)d;
+    for (; g.any(n); g.row += R * g.step) {
+        Raw<T, 8> rx[R][CH], rg[R][CH];
+        f32x2 minus[R], r2[R];
+        float2 s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = g.row + r * g.step;
+            const bool live = at < n;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                rx[r][c].zero();
+                rg[r][c].zero();
+                if (live && column(c) < d) {
+                    rx[r][c].load(x + at * d + column(c));
+                    rg[r][c].load(dy + at * d + column(c));
+                }
+            }
+            const float mean = live ? __ldg(mean_in + at) : 0.f, rstd = live ? __ldg(rstd_in + at) : 0.f;
+            minus[r] = pair(-mean, -mean);
+            r2[r] = pair(rstd, rstd);
+        }
+        f32x2 s1[R], s2[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s1[r] = s2[r] = pair(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (column(c) >= d) continue;
+            f32x2 wv[4];
+            if (w) load_pairs8(w + column(c), wv);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                f32x2 xv[4], gv[4];
+                pairs8(rx[r][c], xv);
+                pairs8(rg[r][c], gv);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 xh = mul2(add2(xv[k], minus[r]), r2[r]);
+                    dw[4 * c + k] = fma2(gv[k], xh, dw[4 * c + k]);
+                    db[4 * c + k] = add2(db[4 * c + k], gv[k]);
+                    if (w) gv[k] = mul2(gv[k], wv[k]);
+                    s1[r] = add2(s1[r], gv[k]);
+                    s2[r] = fma2(gv[k], xh, s2[r]);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r] = make_float2(group_sum<L>(sum2(s1[r])), group_sum<L>(sum2(s2[r])));
+        if (dx == nullptr) continue;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (column(c) >= d) continue;
+            f32x2 wv[4];
+            if (w) load_pairs8(w + column(c), wv);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t at = g.row + r * g.step;
+                if (at >= n) continue;
+                const f32x2 m1 = pair(-s[r].x * inv_d, -s[r].x * inv_d), m2 = pair(-s[r].y * inv_d, -s[r].y * inv_d);
+                f32x2 xv[4], gv[4], out[4];
+                pairs8(rx[r][c], xv);
+                pairs8(rg[r][c], gv);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 xh = mul2(add2(xv[k], minus[r]), r2[r]);
+                    if (w) gv[k] = mul2(gv[k], wv[k]);
+                    out[k] = mul2(fma2(xh, m2, add2(gv[k], m1)), r2[r]);
+                }
+                store_pairs8(dx + at * d + column(c), out);
+            }
+        }
+    }
+    if (part != nullptr)
+        write_columns<T, L, CH, K7_WARPS, true>(dw, db, g, red, part + (int64_t)blockIdx.x * 2 * d, d);
 }
 
 // Column sums of the blocks' partial rows: 32 columns per block, 8 threads
@@ -600,18 +753,22 @@ cudaError_t ln_launch(const LnArgs& a, bool grad, const RowShape& r) {
     const int own = ALIGNED ? 0 : threads * CH * 32;  // a thread's weights
     const int red = L > 0 ? (ALIGNED ? warps : warps * 32 / (L > 0 ? L : 1)) * L * CH * 32 : 0;
     const int smem = grad ? (red > own ? red : own) : 2 * own;
-    const void* kernel = grad ? reinterpret_cast<const void*>(&k7_layernorm_grad<T, TW, L, CH, ALIGNED>)
-                              : reinterpret_cast<const void*>(&k7_layernorm<T, TW, L, CH, ALIGNED>);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+    auto raise = [&](auto* kernel) {
+        if (smem <= 48 * 1024) return cudaSuccess;
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    };
+    auto run_grad = [&](auto* kernel) {
+        if (const cudaError_t e = raise(kernel); e != cudaSuccess) return e;
+        kernel<<<a.grid, threads, smem, a.s>>>(dy, x, w, a.mean, a.rstd, y, a.part, a.n, a.d);
+        return cudaGetLastError();
+    };
+    if (grad) {
+        if constexpr (ALIGNED && L > 0 && CH <= 2) return run_grad(&k7_layernorm_grad_rows<T, TW, L, CH>);
+        else return run_grad(&k7_layernorm_grad<T, TW, L, CH, ALIGNED>);
     }
-    if (grad)
-        k7_layernorm_grad<T, TW, L, CH, ALIGNED><<<a.grid, threads, smem, a.s>>>(dy, x, w, a.mean, a.rstd, y, a.part,
-                                                                                 a.n, a.d);
-    else
-        k7_layernorm<T, TW, L, CH, ALIGNED><<<a.grid, threads, smem, a.s>>>(x, w, bias, y, a.mean, a.rstd, a.n, a.d,
-                                                                            a.eps);
+    const auto kernel = &k7_layernorm<T, TW, L, CH, ALIGNED>;
+    if (const cudaError_t e = raise(kernel); e != cudaSuccess) return e;
+    kernel<<<a.grid, threads, smem, a.s>>>(x, w, bias, y, a.mean, a.rstd, a.n, a.d, a.eps);
     return cudaGetLastError();
 }
 
