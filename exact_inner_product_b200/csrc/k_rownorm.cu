@@ -14,9 +14,9 @@
 // All are HBM-bound: each row is read once into registers, where every sum is
 // taken (the variance from the centred values, not from the sum of squares,
 // which cancels when the mean is large). A row belongs to a group of L lanes
-// of one warp, or to a block when it is too wide for a warp's registers; a
-// group walks over its rows and has the next one's loads in flight while it
-// works on one. The arithmetic is on fp32 pairs (f32x2), which halves the
+// of one warp, or to a block or a team of warps when it is too wide for a warp's
+// registers; a group walks over its rows, and several rows, or the next one, are
+// in flight while it works on one. The arithmetic is on fp32 pairs (f32x2), which halves the
 // instructions that otherwise bound the gradient.
 //
 // Rows travel as 16-byte pieces between memory and registers, 8 elements per
@@ -254,7 +254,7 @@ template <int CH>
 constexpr int grad_rows() { return CH == 1 ? 4 : 2; }
 
 template <typename T, typename TW, int L, int CH, bool ALIGNED>
-__global__ void __launch_bounds__(L > 0 ? K7_THREADS : 512)
+__global__ void __launch_bounds__(L > 0 ? K7_THREADS : CH == 8 ? 320 : 512)
     k7_layernorm(const T* __restrict__ x, const TW* __restrict__ w, const TW* __restrict__ bias, T* __restrict__ y,
                  float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t n, int d, float eps) {
     constexpr int R = forward_rows<L, CH, ALIGNED>();
@@ -407,21 +407,20 @@ __device__ __forceinline__ void write_columns(const f32x2* dw, const f32x2* db, 
 }
 
 template <typename T, typename TW, int L, int CH, bool ALIGNED>
-__global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? grad_resident<CH>() : 1)
+__global__ void __launch_bounds__(32 * grad_warps<CH>(), grad_resident<CH>())
     k7_layernorm_grad(const T* __restrict__ dy, const T* __restrict__ x, const TW* __restrict__ w,
                       const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* __restrict__ dx,
                       float* __restrict__ part, int64_t n, int d) {
     // The next row's loads ahead, where the registers hold them: fp32 rows of four
     // chunks do not fit beside the sums (100000 x 776 fp32 314 against 182 us), nor
     // do unaligned bf16 ones (100000 x 777: 184 against 161 us).
-    constexpr bool AHEAD = CH <= 2 || (L > 0 && ALIGNED && sizeof(T) == 2);
+    constexpr bool AHEAD = CH <= 2 || (ALIGNED && sizeof(T) == 2);
     constexpr int WARPS = grad_warps<CH>();
-    __shared__ float2 sm[2][32];
     extern __shared__ float4 places[];  // the threads' weights; at the end the warps' column sums
     Group<L, WARPS> g;
     const int off = row_offset<T, ALIGNED>(g.row, d);
     const T *x_end = x + n * d, *dy_end = dy + n * d;
-    const Weights<TW, CH, ALIGNED> ww(w, places, g.lane, g.size, off, d);
+    const Weights<TW, CH, ALIGNED> ww(w, places, g.lane, L, off, d);
     f32x2 dw[CH * 4], db[CH * 4];
 #pragma unroll
     for (int i = 0; i < CH * 4; ++i) dw[i] = db[i] = pair(0.f, 0.f);
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
         const bool live = row < n;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int col = (c * g.size + g.lane) * 8 - off;
+            const int col = (c * L + g.lane) * 8 - off;
             nx[c].zero();
             ng[c].zero();
             if (live && col < d) {
@@ -457,7 +456,7 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
             rx[c] = nx[c];
             rg[c] = ng[c];
             if (!ALIGNED) {
-                const uint32_t keep = kept((c * g.size + g.lane) * 8 - off, d);
+                const uint32_t keep = kept((c * L + g.lane) * 8 - off, d);
                 clear_others(rx[c], keep);
                 clear_others(rg[c], keep);
             }
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
         f32x2 s1 = pair(0.f, 0.f), s2 = s1;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int col = (c * g.size + g.lane) * 8 - off;
+            const int col = (c * L + g.lane) * 8 - off;
             if (col >= d) continue;
             f32x2 xv[4], gv[4], wv[4];
             pairs8(rx[c], xv);
@@ -484,12 +483,12 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
                 s2 = fma2(gv[k], xh, s2);
             }
         }
-        const float2 s = g.sums(sum2(s1), sum2(s2), sm);
+        const float2 s = make_float2(group_sum<L>(sum2(s1)), group_sum<L>(sum2(s2)));
         if (!live || dx == nullptr) continue;
         const f32x2 m1 = pair(-s.x * inv_d, -s.x * inv_d), m2 = pair(-s.y * inv_d, -s.y * inv_d);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int col = (c * g.size + g.lane) * 8 - off;
+            const int col = (c * L + g.lane) * 8 - off;
             if (col >= d) continue;
             f32x2 xv[4], gv[4], wv[4], out[4];
             pairs8(rx[c], xv);
@@ -505,23 +504,9 @@ __global__ void __launch_bounds__(L > 0 ? 32 * grad_warps<CH>() : 512, L > 0 ? g
             else store_kept(dx + g.row * d + col, out, kept(col, d));
         }
     }
-    if (part == nullptr) return;
-    float* row = part + (int64_t)blockIdx.x * 2 * d;
-    if constexpr (L > 0) {
-        write_columns<T, L, CH, WARPS, ALIGNED>(dw, db, g, reinterpret_cast<float*>(places), row, d);
-    } else {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int col = (c * g.size + g.lane) * 8 - off;
-            if (col >= d) continue;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 a = unpair(dw[4 * c + k]), b = unpair(db[4 * c + k]);
-                if (col + 2 * k >= 0 && col + 2 * k < d) row[col + 2 * k] = a.x, row[d + col + 2 * k] = b.x;
-                if (col + 2 * k + 1 >= 0 && col + 2 * k + 1 < d) row[col + 2 * k + 1] = a.y, row[d + col + 2 * k + 1] = b.y;
-            }
-        }
-    }
+    if (part != nullptr)
+        write_columns<T, L, CH, WARPS, ALIGNED>(dw, db, g, reinterpret_cast<float*>(places),
+                                                part + (int64_t)blockIdx.x * 2 * d, d);
 }
 
 // The same for narrow rows (a multiple of 8, up to 512 columns), several at once.
@@ -613,6 +598,219 @@ __global__ void __launch_bounds__(K7_THREADS, 2)
         write_columns<T, L, CH, K7_WARPS, true>(dw, db, g, red, part + (int64_t)blockIdx.x * 2 * d, d);
 }
 
+// ---------------------------------------------------------------------------
+// the gradient of wide rows (above 1024 columns): a team of warps per row
+// ---------------------------------------------------------------------------
+// Each thread has CH chunks of a row and keeps their weights and column sums in
+// registers; a team works on R rows at once, whose loads are in flight together
+// and whose sums share a barrier. A block holds as many teams as fit. (A block
+// per row, one row ahead: 30000 x 2400 bf16 145 against 112 us, fp32 250 against
+// 172; 2401 columns 245 against 135 and 282 against 190.)
+template <int CH>
+constexpr int team_threads() { return CH == 8 ? 320 : 512; }
+template <typename T, int CH>
+constexpr int team_rows() { return CH >= 4 ? 1 : (sizeof(T) == 2 ? 4 : 2) / CH; }
+
+struct Team {
+    int lane, size, id, turn;
+    int64_t row, step;
+    float* buf;  // [2][warps][8]
+    __device__ __forceinline__ Team(int threads, float* sm) : size(threads), turn(0) {
+        id = (int)threadIdx.x / size;
+        lane = (int)threadIdx.x - id * size;
+        const int teams = (int)blockDim.x / size;
+        row = (int64_t)blockIdx.x * teams + id;
+        step = (int64_t)gridDim.x * teams;
+        buf = sm + id * (size >> 5) * 16;
+    }
+    // f of the sums of K values over the team, given to every thread. A warp halves
+    // the number of values per lane with each exchange; each lane then adds the
+    // warps' sums of one value, in order, and passes it on. The two buffers
+    // alternate, so one barrier per call suffices.
+    template <int K, typename F>
+    __device__ __forceinline__ void sums(float* v, F f) {
+        const int l = threadIdx.x & 31;
+        int o = 16;
+#pragma unroll
+        for (int half = K / 2; half >= 1; half >>= 1, o >>= 1) {
+            const bool up = l & o;
+#pragma unroll
+            for (int i = 0; i < half; ++i) {
+                const float give = up ? v[i] : v[i + half];
+                v[i] = (up ? v[i + half] : v[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+        }
+#pragma unroll
+        for (int q = 16 / K; q >= 1; q >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], q);
+        float* b = buf + turn * (size >> 5) * 8;
+        turn ^= 1;
+        if ((l & (32 / K - 1)) == 0) b[(lane >> 5) * 8 + l / (32 / K)] = v[0];
+        named_bar_sync(1 + id, size);
+        float s = 0.f;
+        for (int q = 0; q < size >> 5; ++q) s += b[q * 8 + l % K];
+        s = f(s);
+#pragma unroll
+        for (int i = 0; i < K; ++i) v[i] = __shfl_sync(0xffffffffu, s, i);
+    }
+};
+
+// The eight weights at column col, where the row has them.
+template <bool ALIGNED, typename TW>
+__device__ __forceinline__ void load_weights(const TW* w, int col, uint32_t keep, f32x2* v) {
+    if (ALIGNED && keep != 0) {
+        load_pairs8(w + col, v);
+        return;
+    }
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        x[k] = 0.f;
+        if (keep >> k & 1u) {
+            Raw<TW, 1> r;
+            r.load(w + col + k);
+            r.get(x + k);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = pair(x[2 * k], x[2 * k + 1]);
+}
+
+template <typename T, typename TW, int CH, bool ALIGNED>
+__global__ void __launch_bounds__(team_threads<CH>(), 1)
+    k7_layernorm_grad_team(const T* __restrict__ dy, const T* __restrict__ x, const TW* __restrict__ w,
+                           const float* __restrict__ mean_in, const float* __restrict__ rstd_in, T* __restrict__ dx,
+                           float* __restrict__ part, int64_t n, int d, int size) {
+    constexpr int R = team_rows<T, CH>();
+    constexpr bool HELD = CH <= 2;
+    __shared__ float4 sm[team_threads<CH>() / 32 * 4];
+    extern __shared__ float red[];  // the teams' column sums
+    Team t(size, reinterpret_cast<float*>(sm));
+    const int off = row_offset<T, ALIGNED>(t.row, d);
+    const T *x_end = x + n * d, *dy_end = dy + n * d;
+    auto column = [&](int c) { return (c * size + t.lane) * 8 - off; };
+    auto keep = [&](int c) { return ALIGNED ? (column(c) < d ? WHOLE : 0u) : kept(column(c), d); };
+    f32x2 wv[HELD ? CH * 4 : 4], dw[CH * 4], db[CH * 4];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        if (HELD && w) load_weights<ALIGNED>(w, column(c), keep(c), wv + 4 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < CH * 4; ++i) dw[i] = db[i] = pair(0.f, 0.f);
+    const float inv_d = 1.0f / (float)d;
+    for (; t.row < n; t.row += R * t.step) {
+        Raw<T, 8> rx[R][CH], rg[R][CH];
+        float mean[R], rstd[R], s[2 * R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t at = t.row + r * t.step;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                rx[r][c].zero();
+                rg[r][c].zero();
+                if (at < n && keep(c) != 0) {
+                    if constexpr (ALIGNED) {
+                        rx[r][c].load(x + at * d + column(c));
+                        rg[r][c].load(dy + at * d + column(c));
+                    } else {
+                        load_chunk(rx[r][c], x + at * d + column(c), x_end);
+                        load_chunk(rg[r][c], dy + at * d + column(c), dy_end);
+                    }
+                }
+            }
+            mean[r] = at < n ? __ldg(mean_in + at) : 0.f;
+            rstd[r] = at < n ? __ldg(rstd_in + at) : 0.f;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const f32x2 minus = pair(-mean[r], -mean[r]), r2 = pair(rstd[r], rstd[r]);
+            f32x2 s1 = pair(0.f, 0.f), s2 = s1;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (keep(c) == 0) continue;
+                if (!ALIGNED) {
+                    clear_others(rx[r][c], keep(c));
+                    clear_others(rg[r][c], keep(c));
+                }
+                if (!HELD && w) load_weights<ALIGNED>(w, column(c), keep(c), wv);
+                const f32x2* wc = wv + (HELD ? 4 * c : 0);
+                f32x2 xv[4], gv[4];
+                pairs8(rx[r][c], xv);
+                pairs8(rg[r][c], gv);  // zeros outside the row, so what xhat is there does not matter
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 xh = mul2(add2(xv[k], minus), r2);
+                    dw[4 * c + k] = fma2(gv[k], xh, dw[4 * c + k]);
+                    db[4 * c + k] = add2(db[4 * c + k], gv[k]);
+                    if (w) gv[k] = mul2(gv[k], wc[k]);
+                    s1 = add2(s1, gv[k]);
+                    s2 = fma2(gv[k], xh, s2);
+                }
+            }
+            s[2 * r] = sum2(s1);
+            s[2 * r + 1] = sum2(s2);
+        }
+        if (dx == nullptr) continue;
+        t.template sums<2 * R>(s, [&](float v) { return -v * inv_d; });
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            if (keep(c) == 0) continue;
+            if (!HELD && w) load_weights<ALIGNED>(w, column(c), keep(c), wv);
+            const f32x2* wc = wv + (HELD ? 4 * c : 0);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int64_t at = t.row + r * t.step;
+                if (at >= n) continue;
+                const f32x2 minus = pair(-mean[r], -mean[r]), r2 = pair(rstd[r], rstd[r]);
+                const f32x2 m1 = pair(s[2 * r], s[2 * r]), m2 = pair(s[2 * r + 1], s[2 * r + 1]);
+                f32x2 xv[4], gv[4], out[4];
+                pairs8(rx[r][c], xv);
+                pairs8(rg[r][c], gv);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 xh = mul2(add2(xv[k], minus), r2);
+                    if (w) gv[k] = mul2(gv[k], wc[k]);
+                    out[k] = mul2(fma2(xh, m2, add2(gv[k], m1)), r2);
+                }
+                if constexpr (ALIGNED) store_pairs8(dx + at * d + column(c), out);
+                else store_kept(dx + at * d + column(c), out, keep(c));
+            }
+        }
+    }
+    if (part == nullptr) return;
+    float* row = part + (int64_t)blockIdx.x * 2 * d;
+    const int teams = (int)blockDim.x / size;
+    if (teams == 1) {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 a = unpair(dw[4 * c + k]), b = unpair(db[4 * c + k]);
+                float* at = row + column(c) + 2 * k;
+                if (keep(c) >> (2 * k) & 1u) at[0] = a.x, at[d] = b.x;
+                if (keep(c) >> (2 * k + 1) & 1u) at[1] = a.y, at[d + 1] = b.y;
+            }
+        }
+        return;
+    }
+    // the teams' sums in order
+    const int width = size * CH * 8;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < CH * 4; ++i)
+            *reinterpret_cast<float2*>(red + t.id * width + (i / 4 * size + t.lane) * 8 + i % 4 * 2) =
+                unpair(which == 0 ? dw[i] : db[i]);
+        __syncthreads();
+        for (int e = threadIdx.x; e < d; e += blockDim.x) {
+            float sum = 0.f;
+            for (int q = 0; q < teams; ++q)
+                sum += red[q * width + e + row_offset<T, ALIGNED>((int64_t)blockIdx.x * teams + q, d)];
+            row[which * d + e] = sum;
+        }
+    }
+}
+
 // Column sums of the blocks' partial rows: 32 columns per block, 8 threads
 // per column over the rows, then those in order. part is [rows][2 d]: dw, db.
 __global__ void __launch_bounds__(256)
@@ -695,14 +893,18 @@ int grid_for(int64_t units, int per_block, int cap) {
 }
 
 // How a layer-norm row is laid on threads: L lanes of a warp (0: a block of
-// `threads`), CH chunks of 8 elements per thread. Up to 1024 columns a warp per
-// row is faster than a block (1000 bf16 columns: 65 against 91 us forward).
+// `threads`; the gradient's team of `threads`), CH chunks of 8 elements per
+// thread. Up to 1024 columns a warp per row is faster than a block (1000 bf16
+// columns: 65 against 91 us forward) or a team (65536 x 1000 bf16 85 against 104 us
+// back). Forward the team is not faster (16384 x 4096 bf16 84, a block 75).
 struct RowShape {
     bool aligned;
     int L, CH, threads;
+    // the wide rows' gradient: teams of `threads` per block
+    int teams() const { return threads < 512 ? 512 / threads : 1; }
 };
 
-RowShape layernorm_shape(int d) {
+RowShape layernorm_shape(int d, bool grad) {
     RowShape r;
     r.aligned = d % 8 == 0;
     r.threads = K7_THREADS;
@@ -713,20 +915,27 @@ RowShape layernorm_shape(int d) {
     r.CH = chunks <= 64 ? 2 : 4;
     if (chunks <= 128) return r;
     r.L = 0;
-    r.CH = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
-    if (chunks > 1024) r.threads = 512;
-    if (chunks > 2048) r.CH = 8;  // 16384 columns that are no multiple of 8
+    if (grad || chunks > 2048) {  // 8 chunks: 16384 columns that are no multiple of 8
+        r.CH = chunks <= 256 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
+        r.threads = (chunks + 32 * r.CH - 1) / (32 * r.CH) * 32;
+    } else {
+        r.CH = chunks <= 256 ? 1 : chunks <= 512 ? 2 : 4;
+        if (chunks > 1024) r.threads = 512;
+    }
     return r;
 }
 
-// Blocks of a kernel with a row per block: rows of one block agree modulo 8.
-int row_blocks(int64_t n, int cap) {
-    const int g = grid_for(n, 1, cap);
-    return g < n ? g / 8 * 8 : g;
+// Blocks of `teams` rows each: rows of a team agree modulo 8, unless they are aligned.
+int row_blocks(int64_t n, int teams, int cap, bool aligned) {
+    const int g = grid_for(n, teams, cap);
+    if (aligned || (int64_t)g * teams >= n) return g;
+    int every = 8;  // a multiple of this many blocks
+    for (int t = teams; every > 1 && t % 2 == 0; t /= 2) every /= 2;
+    return g / every * every;
 }
 
 int grad_blocks(int64_t n, const RowShape& r, int sm_count) {
-    if (r.L == 0) return row_blocks(n, (r.CH == 1 ? 1024 : r.CH == 2 ? 768 : 512) / r.threads * sm_count / 8 * 8);
+    if (r.L == 0) return row_blocks(n, r.teams(), sm_count, r.aligned);
     if (r.CH < 4) return grid_for(n, grad_warps<1>() * (32 / r.L), grad_resident<1>() * sm_count);
     // an even number, so that a warp's rows agree modulo 8
     return grid_for(n, grad_warps<4>(), grad_resident<4>() * (sm_count / 2 * 2));
@@ -763,8 +972,17 @@ cudaError_t ln_launch(const LnArgs& a, bool grad, const RowShape& r) {
         return cudaGetLastError();
     };
     if (grad) {
-        if constexpr (ALIGNED && L > 0 && CH <= 2) return run_grad(&k7_layernorm_grad_rows<T, TW, L, CH>);
-        else return run_grad(&k7_layernorm_grad<T, TW, L, CH, ALIGNED>);
+        if constexpr (L == 0) {
+            const int block = r.teams() * r.threads;
+            const int sums = r.teams() > 1 ? block * CH * 32 : 0;
+            k7_layernorm_grad_team<T, TW, CH, ALIGNED><<<a.grid, block, sums, a.s>>>(dy, x, w, a.mean, a.rstd, y,
+                                                                                     a.part, a.n, a.d, r.threads);
+            return cudaGetLastError();
+        } else if constexpr (ALIGNED && CH <= 2) {
+            return run_grad(&k7_layernorm_grad_rows<T, TW, L, CH>);
+        } else {
+            return run_grad(&k7_layernorm_grad<T, TW, L, CH, ALIGNED>);
+        }
     }
     const auto kernel = &k7_layernorm<T, TW, L, CH, ALIGNED>;
     if (const cudaError_t e = raise(kernel); e != cudaSuccess) return e;
@@ -822,14 +1040,14 @@ void normalize_grad_shape(const void* dy, const void* x, void* dx, int64_t n, in
 }  // namespace
 
 size_t layernorm_grad_bytes(int64_t n, int d, int sm_count) {
-    return (size_t)grad_blocks(n, layernorm_shape(d), sm_count) * 2 * d * sizeof(float);
+    return (size_t)grad_blocks(n, layernorm_shape(d, true), sm_count) * 2 * d * sizeof(float);
 }
 
 cudaError_t launch_layernorm(const void* x, int x_dtype, int64_t n, int d, const void* w, const void* bias,
                              int w_dtype, float eps, void* y, float* mean, float* rstd, cudaStream_t s, int sm_count) {
-    const RowShape r = layernorm_shape(d);
+    const RowShape r = layernorm_shape(d, false);
     // unaligned rows: blocks that stay, for their weights are loaded first
-    const int grid = r.L == 0 ? row_blocks(n, (r.aligned ? 2048 : 1024) / r.threads * sm_count / 8 * 8)
+    const int grid = r.L == 0 ? row_blocks(n, 1, (r.aligned ? 2048 : 1024) / r.threads * sm_count, r.aligned)
                               : grid_for(n, K7_WARPS * (32 / r.L), (r.aligned ? 32 : 6) * sm_count);
     const LnArgs a = {nullptr, x, w, bias, y, mean, rstd, nullptr, n, d, eps, grid, s};
     return ln_dispatch(a, x_dtype, w_dtype, false, r);
@@ -838,7 +1056,7 @@ cudaError_t launch_layernorm(const void* x, int x_dtype, int64_t n, int d, const
 cudaError_t launch_layernorm_grad(const void* dy, const void* x, int x_dtype, int64_t n, int d, const void* w,
                                   int w_dtype, const float* mean, const float* rstd, void* dx, float* dw, float* db,
                                   float* part, cudaStream_t s, int sm_count) {
-    const RowShape r = layernorm_shape(d);
+    const RowShape r = layernorm_shape(d, true);
     const bool columns = dw != nullptr || db != nullptr;
     const int grid = grad_blocks(n, r, sm_count);
     const LnArgs a = {dy, x, w, nullptr, dx, const_cast<float*>(mean), const_cast<float*>(rstd),

@@ -80,6 +80,29 @@ def test_layernorm_many_rows(n, d):
     assert all(torch.equal(a, b) for a, b in zip(got, again))  # the same bits on every run
 
 
+@pytest.mark.parametrize("n,d", [(2000, 1536), (1999, 2401), (2600, 1033), (700, 4097), (450, 8192), (310, 12288), (5, 16378),
+                                 (301, 16383)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layernorm_wide_rows(n, d, dtype):
+    """Several rows per team of warps, one to three teams per block, and the
+    widest rows that do not begin on 16 bytes; also without weights."""
+    _cuda()
+    g = _gen(n + d)
+    x, dy = _rows(g, n, d, dtype), _rows(g, n, d, dtype, spread=False)
+    w = (1 + 0.5 * torch.randn(d, generator=g, device="cuda"))
+    y, mean, rstd = tt.tt_layernorm(x, w, None, 1e-5)
+    (y8, _, _), (ey, _, _) = R.layernorm(x, w, None, 1e-5)
+    R.close(y, y8, ey + (y8.abs() + ey) * R.half_step(dtype), "y")
+    for weights in (w, None):
+        got = tt.tt_layernorm_grad(dy, x, weights, mean, rstd)
+        want, tol = R.layernorm_grad(dy, x, weights, mean, rstd)
+        R.close(got[0], want[0], tol[0] + (want[0].abs() + tol[0]) * R.half_step(dtype), "grad_x")
+        R.close(got[1], want[1], tol[1], "grad_w")
+        R.close(got[2], want[2], tol[2], "grad_bias")
+    sums = tt.tt_layernorm_grad(dy, x, None, mean, rstd, out=(None, torch.empty_like(got[1]), torch.empty_like(got[2])))
+    assert torch.equal(sums[1], got[1]) and torch.equal(sums[2], got[2])
+
+
 def test_layernorm_without_weights_and_parts():
     _cuda()
     g = _gen(3)
