@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(K9_THREADS)
     const float norm = total_norm(part, parts, sm);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
     const float ratio = max_norm / (norm + 1e-6f);
-    const float scale = ratio >= 1.0f ? 1.0f : ratio;  // NaN stays
+    // NaN stays, but no limit is not exceeded by an infinite norm
+    const float scale = ratio >= 1.0f || (isinf(max_norm) && isinf(norm)) ? 1.0f : ratio;
     int lo, hi;
     block_range(t.chunks, &lo, &hi);
     if (lo >= hi) return;

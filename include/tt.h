@@ -496,7 +496,7 @@ TT_API tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const v
  * The squares are summed in fp64 (groups of eight in fp32 where they neither
  * overflow nor underflow there); norm and scale are fp32. A norm that is NaN
  * makes every element NaN, an infinite one makes scale 0 (and an infinite
- * element NaN), as the formula says.
+ * element NaN), as the formula says; scale is 1 if max_norm is infinite too.
  *
  * count      tensors, >= 0 (0: the norm is 0)
  * grads      HOST array of device pointers, aligned to their element size

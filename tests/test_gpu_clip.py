@@ -119,6 +119,16 @@ def test_not_finite():
     assert float(tt.tt_clip_grad_norm(zeros, 1.0)) == 0.0 and bool((zeros[0] == 0).all())
 
 
+def test_no_limit_and_an_infinite_norm():
+    """An infinite max_norm only measures: the tensors stay as they are."""
+    _cuda()
+    grads = _tensors([(100, F32), (100, BF16)])
+    grads[1][3] = float("inf")
+    before = [t.clone() for t in grads]
+    assert float(tt.tt_clip_grad_norm(grads, float("inf"))) == math.inf
+    assert all(torch.equal(a, b) for a, b in zip(grads, before))
+
+
 def test_tensor_past_2_31_elements():
     _cuda()
     t = torch.zeros((1 << 31) + 9, dtype=BF16, device="cuda")

@@ -113,6 +113,20 @@ def test_gradient_widths(d, dtype, out_dtype, idt):
     _check_grad(ids, grad, rows, 0.5, out_dtype)
 
 
+@pytest.mark.parametrize("d", [1001, 2049, 4096, 8190, 16383, 16384])
+@pytest.mark.parametrize("dtype,out_dtype", [(F32, F32), (BF16, BF16)])
+def test_wide_rows(d, dtype, out_dtype):
+    _cuda()
+    g = _gen(d)
+    rows, m = 19, 300
+    ids = torch.randint(-1, rows, (m,), generator=g, device="cuda")
+    grad = torch.randn((m, d), generator=g, device="cuda").to(dtype)
+    _check_grad(ids, grad, rows, 1.0, out_dtype)
+    table = torch.randn((rows, d), generator=g, device="cuda").to(dtype)
+    want = torch.where((ids >= 0)[:, None], table[ids.clamp(min=0)], torch.zeros((), dtype=dtype, device="cuda"))
+    assert torch.equal(tt.tt_embedding(table, ids), want)
+
+
 # one token, one warp-chunk and one more, a block's sort and one more, tiles of the larger sort
 LENGTHS = [1, 2, 31, 32, 33, 64, 255, 1023, 1025, 4096, 4097, 16383, 16384, 16385, 20480, 40001]
 
