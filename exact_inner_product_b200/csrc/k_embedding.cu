@@ -337,11 +337,15 @@ struct OneSmem {
 };
 
 // Block 0 sorts; the others set the `zeros` 16-byte pieces at `zero` (and the
-// last `tail` bytes), for the dense gradient's rows without a token.
-template <typename ID, int THREADS>
+// last `tail` bytes), for the dense gradient's rows without a token. For the form
+// by rows block 0 also counts the runs (`count`), and
+// those before each K8_RUN tokens (`place`; `first` is zero, see k8_heads): two
+// launches less.
+template <typename ID, int THREADS, bool BY_ROW>
 __global__ void __launch_bounds__(THREADS)
     k8_sort_one(const ID* __restrict__ ids, int m, uint32_t rows, int passes, int bits, uint2* __restrict__ out,
-                int* __restrict__ cross_count, uint4* __restrict__ zero, int64_t zeros, int tail) {
+                int* __restrict__ cross_count, uint4* __restrict__ zero, int64_t zeros, int tail,
+                int32_t* __restrict__ place, int32_t* __restrict__ first, int32_t* __restrict__ count) {
     constexpr int PARTS = THREADS / K8_BINS;           // threads per digit
     constexpr int PER = THREADS / 32 / PARTS;          // warps whose counts a thread adds
     extern __shared__ __align__(16) uint8_t raw[];
@@ -434,7 +438,40 @@ __global__ void __launch_bounds__(THREADS)
         }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < m; i += THREADS) out[i] = make_uint2(sm.key[passes & 1][i], sm.pos[passes & 1][i]);
+    const uint32_t* key = sm.key[passes & 1];
+    for (int i = threadIdx.x; i < m; i += THREADS) out[i] = make_uint2(key[i], sm.pos[passes & 1][i]);
+    if constexpr (!BY_ROW) return;
+    constexpr int PER_LANE = THREADS * K8_KEYS / K8_RUN / 32;
+    const int chunks = (m + K8_RUN - 1) / K8_RUN;
+    int* runs = reinterpret_cast<int*>(sm.cnt);
+    for (int c = warp; c < chunks; c += THREADS / 32) {
+        const int i = c * K8_RUN + lane;
+        const bool head = i < m && key[i] < rows && (i == 0 || key[i - 1] != key[i]);
+        const unsigned heads = __ballot_sync(0xffffffffu, head);
+        if (lane == 0) runs[c] = __popc(heads);
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    int own[PER_LANE], sum = 0;
+#pragma unroll
+    for (int q = 0; q < PER_LANE; ++q) {
+        own[q] = lane * PER_LANE + q < chunks ? runs[lane * PER_LANE + q] : 0;
+        sum += own[q];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    int before = inc - sum;
+#pragma unroll
+    for (int q = 0; q < PER_LANE; ++q) {
+        if (lane * PER_LANE + q < chunks) place[lane * PER_LANE + q] = before;
+        before += own[q];
+    }
+    if (lane < (m + K8_HEADS - 1) / K8_HEADS) first[lane] = 0;
+    if (lane == 31) *count = inc;
 }
 
 // ---------------------------------------------------------------------------
@@ -805,10 +842,11 @@ GradPlan grad_plan(int64_t m, int64_t rows, int d) {
 }
 
 // Sorts the tokens into *sorted. The sort of one block also sets `bytes` of
-// zeros at `zero`; the other one leaves that to the caller.
+// zeros at `zero` and counts the runs where `count` is given; the other one
+// leaves both to the caller.
 template <typename ID>
 cudaError_t sort_tokens(const GradPlan& p, const void* ids, int64_t m, uint32_t rows, uint8_t* ws, void* zero,
-                        size_t bytes, cudaStream_t s, int sm_count, const uint2** sorted) {
+                        size_t bytes, int32_t* count, cudaStream_t s, int sm_count, const uint2** sorted) {
     uint2* tok[2] = {reinterpret_cast<uint2*>(ws + p.off_tok[0]), reinterpret_cast<uint2*>(ws + p.off_tok[1])};
     int* cross_count = reinterpret_cast<int*>(ws + p.off_cross_count);
     cudaError_t e;
@@ -824,12 +862,16 @@ cudaError_t sort_tokens(const GradPlan& p, const void* ids, int64_t m, uint32_t 
             note_launch_begin(TT_KIND_EMBEDDING, s);
             kernel<<<grid, threads, smem, s>>>(static_cast<const ID*>(ids), (int)m, rows, p.passes, p.bits, tok[0],
                                                cross_count, static_cast<uint4*>(zero), (int64_t)(bytes / 16),
-                                               (int)(bytes % 16));
+                                               (int)(bytes % 16), reinterpret_cast<int32_t*>(ws + p.off_place),
+                                               reinterpret_cast<int32_t*>(ws + p.off_first), count);
             note_launch_end(TT_KIND_EMBEDDING, s);
             return cudaGetLastError();
         };
-        return threads == 256 ? launch(k8_sort_one<ID, 256>, sizeof(OneSmem<256>))
-                              : launch(k8_sort_one<ID, 512>, sizeof(OneSmem<512>));
+        if (threads == 256)
+            return count != nullptr ? launch(k8_sort_one<ID, 256, true>, sizeof(OneSmem<256>))
+                                    : launch(k8_sort_one<ID, 256, false>, sizeof(OneSmem<256>));
+        return count != nullptr ? launch(k8_sort_one<ID, 512, true>, sizeof(OneSmem<512>))
+                                : launch(k8_sort_one<ID, 512, false>, sizeof(OneSmem<512>));
     }
     SortArgs a;
     a.hist = reinterpret_cast<int32_t*>(ws + p.off_hist);
@@ -875,7 +917,8 @@ cudaError_t embedding_grad_ids(const EmbeddingGrad& g, bool by_row, cudaStream_t
     if (zeros > 0 && (g.m > K8_ONE || g.m == 0) && (e = cudaMemsetAsync(g.out, 0, zeros, s)) != cudaSuccess) return e;
     if (g.m == 0) return by_row ? cudaMemsetAsync(g.count, 0, sizeof(int32_t), s) : cudaSuccess;
     RunArgs a;
-    if ((e = sort_tokens<ID>(p, g.ids, g.m, (uint32_t)g.rows, ws, g.out, zeros, s, sm_count, &a.tok)) != cudaSuccess)
+    if ((e = sort_tokens<ID>(p, g.ids, g.m, (uint32_t)g.rows, ws, g.out, zeros, by_row ? g.count : nullptr, s, sm_count,
+                             &a.tok)) != cudaSuccess)
         return e;
     a.m = g.m;
     a.rows = (uint32_t)g.rows;
@@ -889,7 +932,7 @@ cudaError_t embedding_grad_ids(const EmbeddingGrad& g, bool by_row, cudaStream_t
     a.cross = reinterpret_cast<int2*>(ws + p.off_cross);
     a.cross_count = reinterpret_cast<int*>(ws + p.off_cross_count);
     a.chunks = p.chunks;
-    if (by_row) {
+    if (by_row && g.m > K8_ONE) {
         note_launch_begin(TT_KIND_EMBEDDING, s);
         e = launch_pdl(k8_heads, dim3((unsigned)p.heads), dim3(K8_HEADS_THREADS), 0, s, a, first);
         note_launch_end(TT_KIND_EMBEDDING, s);
