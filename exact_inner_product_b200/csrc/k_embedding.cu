@@ -21,6 +21,9 @@
 //                  joins what its eight warps hold of one run, and writes it; the
 //                  part of a run that reaches past the block goes to a partial row
 //   k8_join        the partial rows of each such run, in order
+// The kernels' launches overlap, so a block may be there before the data that it
+// reads: what an earlier kernel of the call writes is read past L1 (__ldcg), whose
+// lines another kernel of the call may have filled before that write.
 // The order of every sum is fixed by the ids, so the bits repeat. Bound by the
 // reading of g (once, in rows) and, for few tokens, by the launches.
 #include <cuda_bf16.h>
@@ -201,7 +204,7 @@ struct SortArgs {
 template <typename ID>
 __device__ __forceinline__ uint2 load_token(const SortArgs& a, int64_t i) {
     if (a.ids != nullptr) return make_uint2(key_of(__ldg(static_cast<const ID*>(a.ids) + i), a.rows), (uint32_t)i);
-    return __ldg(a.in + i);
+    return __ldcg(a.in + i);
 }
 
 template <typename ID>
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(256) k8_scan(int32_t* __restrict__ x, int len,
     int run = 0;
     for (int base = 0; base < len; base += 256) {
         const int i = base + threadIdx.x;
-        const int v = i < len ? row[i] : 0;
+        const int v = i < len ? __ldcg(row + i) : 0;
         int inc = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -305,13 +308,13 @@ __global__ void __launch_bounds__(K8_SORT_THREADS) k8_scatter(const SortArgs a) 
     if (a.tiles <= K8_FEW_TILES) {
 #pragma unroll 16
         for (int t = 0; t < a.tiles; ++t) {
-            const int c = __ldg(a.hist + t * K8_BINS + threadIdx.x);
+            const int c = __ldcg(a.hist + t * K8_BINS + threadIdx.x);
             all += c;
             if (t < blockIdx.x) earlier += c;
         }
     } else {
-        all = __ldg(a.total + threadIdx.x);
-        earlier = __ldg(a.hist + (int64_t)threadIdx.x * a.tiles + blockIdx.x);
+        all = __ldcg(a.total + threadIdx.x);
+        earlier = __ldcg(a.hist + (int64_t)threadIdx.x * a.tiles + blockIdx.x);
     }
     const int before = block_prefix256(all, warp_tot[0]);  // has a barrier
     int sum = 0;
@@ -508,7 +511,7 @@ struct RunArgs {
     int2* cross;           // runs that go on past their block: (block, output row)
     int* cross_count;
     int64_t chunks;        // of 32 tokens
-    __device__ __forceinline__ uint32_t key(int64_t i) const { return __ldg(&tok[i].x); }
+    __device__ __forceinline__ uint32_t key(int64_t i) const { return __ldcg(&tok[i].x); }
 };
 
 __device__ __forceinline__ bool is_head(const RunArgs& a, int64_t i) {
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(K8_RUN_WARPS * 32)
     pdl_wait();
     const int64_t i0 = chunk * K8_RUN;
     const int64_t i = i0 + lane;
-    const uint2 tok = i < a.m ? __ldg(a.tok + i) : make_uint2(a.rows, 0u);
+    const uint2 tok = i < a.m ? __ldcg(a.tok + i) : make_uint2(a.rows, 0u);
     const uint32_t key = tok.x;
     uint32_t prev = __shfl_up_sync(0xffffffffu, key, 1);
     if (lane == 0) prev = i0 > 0 && i0 < a.m ? a.key(i0 - 1) : a.rows;
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(K8_RUN_WARPS * 32)
     const bool goes_on = count == 32 && i0 + 32 < a.m && a.key(i0 + 32) == last_key;
     int64_t first = 0;  // place of the first run that begins here
     if (a.by_row && count > 0)
-        first = (int64_t)__ldg(a.block_first + chunk / K8_HEADS_CHUNKS) + __ldg(a.place + chunk);
+        first = (int64_t)__ldcg(a.block_first + chunk / K8_HEADS_CHUNKS) + __ldcg(a.place + chunk);
     const int e = (blockIdx.y * 32 * K + lane) * E;
     if (out_ids != nullptr && blockIdx.y == 0 && (heads >> lane & 1u))
         out_ids[first + __popc(heads & ((1u << lane) - 1u))] = (ID)key;
@@ -673,6 +676,26 @@ __global__ void __launch_bounds__(K8_RUN_WARPS * 32)
     }
 }
 
+// A lane's part of a partial row, past L1.
+__device__ __forceinline__ void load_part(Raw<float, 1>& r, const float* p) { r.a = __ldcg(p); }
+__device__ __forceinline__ void load_part(Raw<float, 2>& r, const float* p) {
+    r.a = __ldcg(reinterpret_cast<const float2*>(p));
+}
+__device__ __forceinline__ void load_part(Raw<float, 4>& r, const float* p) {
+    r.a = __ldcg(reinterpret_cast<const float4*>(p));
+}
+__device__ __forceinline__ void load_part(Raw<float, 8>& r, const float* p) {
+    r.a = __ldcg(reinterpret_cast<const float4*>(p));
+    r.b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+}
+template <int E, int K>
+__device__ __forceinline__ void load_part(Strip<float, E, K>& s, const float* row, int e, int d) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        if (e + j * 32 * E < d) load_part(s.r[j], row + e + j * 32 * E); else s.r[j].zero();
+    }
+}
+
 // A run that begins in block c and goes on: its own partial row (slot 1 of c),
 // then slot 0 of the blocks after c that it reaches. A warp adds up to
 // K8_JOIN_WARP of them; longer runs take the whole block, warp w the blocks
@@ -690,7 +713,7 @@ __device__ __forceinline__ void add_parts(const RunArgs& a, int64_t c, int64_t f
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
             const int64_t k = k0 + (int64_t)q * step;
-            if (k < to) r[q].load(a.part + (c + k) * 2 * a.d, e, 32 * E, a.d); else r[q].zero();
+            if (k < to) load_part(r[q], a.part + (c + k) * 2 * a.d, e, a.d); else r[q].zero();
         }
 #pragma unroll
         for (int q = 0; q < BATCH; ++q) {
@@ -709,7 +732,7 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
     __shared__ float sums[K8_JOIN_WARPS][N][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    const int n = *a.cross_count;
+    const int n = __ldcg(a.cross_count);
     const int e = (blockIdx.y * 32 * K + lane) * E;
     // Neighbours in the list go to different blocks: the longest runs, of the
     // lowest ids where those are the popular ones, stand side by side.
@@ -717,7 +740,7 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
     for (int b = blockIdx.x; b < n; b += grid * K8_JOIN_WARPS) {
         int64_t k = 0;  // blocks after the first that the run reaches
         if (b + warp * grid < n) {
-            const int64_t c = a.cross[b + warp * grid].x;
+            const int64_t c = __ldcg(&a.cross[b + warp * grid].x);
             const uint32_t key = a.key(c * K8_BLOCK + K8_BLOCK - 1);
             while (true) {
                 const int64_t i = (c + 1 + k + lane) * K8_BLOCK;
@@ -730,10 +753,10 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
         if (lane == 0) reach[warp] = k;
         __syncthreads();
         if (k > 0 && k <= K8_JOIN_WARP) {
-            const int2 run = a.cross[b + warp * grid];
+            const int2 run = __ldcg(a.cross + b + warp * grid);
             float acc[N];
             Strip<float, E, K> r;
-            r.load(a.part + ((int64_t)run.x * 2 + 1) * a.d, e, 32 * E, a.d);
+            load_part(r, a.part + ((int64_t)run.x * 2 + 1) * a.d, e, a.d);
             r.get(acc);
             add_parts<E, K>(a, run.x, 1, k + 1, 1, e, acc);
 #pragma unroll
@@ -743,13 +766,13 @@ __global__ void __launch_bounds__(K8_JOIN_WARPS * 32) k8_join(const RunArgs a, T
         for (int w = 0; w < K8_JOIN_WARPS; ++w) {
             const int64_t kw = reach[w];
             if (kw <= K8_JOIN_WARP) continue;  // the same for the whole block
-            const int2 run = a.cross[b + w * grid];
+            const int2 run = __ldcg(a.cross + b + w * grid);
             float acc[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) acc[j] = 0.f;
             if (warp == 0) {
                 Strip<float, E, K> r;
-                r.load(a.part + ((int64_t)run.x * 2 + 1) * a.d, e, 32 * E, a.d);
+                load_part(r, a.part + ((int64_t)run.x * 2 + 1) * a.d, e, a.d);
                 r.get(acc);
             }
             add_parts<E, K>(a, run.x, 1 + warp, kw + 1, K8_JOIN_WARPS, e, acc);

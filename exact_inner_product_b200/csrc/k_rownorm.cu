@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(256)
     float s = 0.f;
     if (col < 2 * d)
 #pragma unroll 8
-        for (int r = ry; r < rows; r += 8) s += __ldg(part + (int64_t)r * 2 * d + col);
+        for (int r = ry; r < rows; r += 8) s += __ldcg(part + (int64_t)r * 2 * d + col);
     sm[ry][cx] = s;
     __syncthreads();
     if (ry == 0 && col < 2 * d) {

@@ -667,7 +667,9 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
         const float* src = p.part + ((int64_t)(uid + first) * K6_M + i % K6_M) * p.width + c8;
 #pragma unroll 4
         for (int c = 0; c < parts; ++c, src += (int64_t)K6_M * p.width) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(src)), y = __ldg(reinterpret_cast<const float4*>(src) + 1);
+            // past L1: written by the kernel before, beside which this one may have started
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + 1);
             acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
             acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
         }
