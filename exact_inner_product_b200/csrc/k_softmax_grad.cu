@@ -25,25 +25,37 @@
 //                tensor cores, turns them into P in registers, writes P as
 //                bf16 over the logits in tensor memory and multiplies it from
 //                there with the tile of rows that is still in shared memory
-//   k6_finish    adds the partial products of each row, the diagonal, and the
-//                scale, and rounds to bf16
+//   k6_finish    adds the partial products of each row, scales them by its sums
+//                of P, adds the diagonal, applies the loss's scale, and rounds to
+//                bf16
 //
 // P is rounded to bf16 (at most a relative 2^-8 of each term, of either sign):
-// its products with bf16 rows are then exact and add in fp32, and what the
-// rounding leaves is of the size of the result's own rounding to bf16.
+// its products with bf16 rows are then exact and add in fp32. The gradient of a
+// user is a sum over differences v_j - v_i (and that of an item nearly one over
+// differences of users), so what the vectors have in common cancels between the
+// product and the diagonal, but only if the coefficients add up to what they did
+// before the rounding: the P of a flat softmax are near one another and may all be
+// rounded the same way, and 2^-8 of a large common component is more than the
+// result. So the epilogue also adds each row's P before and after the rounding, in
+// fp32, and k6_finish scales the row's product by the ratio of the two sums. What
+// the rounding then leaves goes by the spread of the rows that are added, at most
+// 2^-7 of sum P |v_j - mean|. The scale is held to 1 / (1 +- 2^-8), which it does
+// not leave where the terms have one sign; weights of both signs can bring the
+// sums near zero.
 // Recomputing the logits in both passes costs 2 of the 8 b nc d operations and
 // a second exponential per logit; one pass would need either atomic additions
 // of b x d (or nc x d) sums per tile, whose order changes the result, or
 // their partial sums in HBM (2.1 GB at 16384 x 32768 x 128).
 //
 // Bound by the tensor cores for d >= 128 and by the exponentials below; the
-// epilogue (about 4 instructions per logit, 2 more with item ids) overlaps with
-// both by two groups of warps and two to three logit tiles in flight. Measured
-// on a B200, 8 b nc d operations in k6_products: 16384 x 32768 x 128 412 us
-// (1.33 PFLOP/s) without masks, 460 us with all; 16384^2 x 256 429 us (1.28);
-// 32768^2 x 64 without masks 686 us (3.1 T exponentials/s); 8192^2 x 512 687 us
-// (one stage of rows fits beside the kept tile, and the logits are formed for
-// each half of the columns).
+// epilogue (about 6 instructions per logit, 2 of them the sums of P, and 2 more
+// with item ids) overlaps with both by two groups of warps and two to three logit
+// tiles in flight. Measured on a B200, 8 b nc d operations in k6_products: 16384 x
+// 32768 x 128 456 us (1.21 PFLOP/s) without masks, 498 us with all (without the
+// sums of P 418 and 459); 16384^2 x 256 412 us (1.33); 32768^2 x 64 without masks
+// 789 us (2.7 T exponentials/s; without the sums 682); 8192^2 x 512 668 us (one
+// stage of rows fits beside the kept tile, and the logits are formed for each half
+// of the columns).
 //
 // The tiles of both passes, row tile after row tile, form one line that is cut
 // evenly among the SMs, so a few row tiles with long sums use the whole GPU
@@ -134,6 +146,7 @@ struct K6Params {
     K6Side user;          // [b]
     const float* weight;  // [b] w_i, padded
     float* part;          // [units + grid][128][width] partial products
+    float* sums;          // [units + grid][K6_GROUPS][2][128] sums of P, before and after its rounding
     int* err;
     int b, nc, d;
     float a2;             // log2(e) / tau
@@ -269,6 +282,37 @@ struct Ring {
             phase ^= 1;
         }
     }
+};
+
+// A thread's sum of one row's P after the rounding, two at a time. Mixed additions
+// (fp32 + bf16) where the test for hits keeps the integer pipe busy, else the bf16
+// pair unpacked and a packed addition (16384 x 32768 x 128 with all masks 532
+// against 551 us a call, without masks 490 against 481; 32768^2 x 64 836 against 811).
+template <bool MIXED>
+struct RoundedSum;
+template <>
+struct RoundedSum<false> {
+    f32x2 s;
+    __device__ __forceinline__ RoundedSum() : s(pair(0.f, 0.f)) {}
+    __device__ __forceinline__ void add(uint32_t bits) {
+        s = add2(s, pair(__uint_as_float(bits << 16), __uint_as_float(bits & 0xFFFF0000u)));
+    }
+    __device__ __forceinline__ float total() const {
+        const float2 v = unpair(s);
+        return v.x + v.y;
+    }
+};
+template <>
+struct RoundedSum<true> {
+    float s;
+    __device__ __forceinline__ RoundedSum() : s(0.f) {}
+    __device__ __forceinline__ void add(uint32_t bits) {
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
+            "add.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %0, hi, %0;\n\t}"
+            : "+f"(s)
+            : "r"(bits));
+    }
+    __device__ __forceinline__ float total() const { return s; }
 };
 
 template <int K>
@@ -497,6 +541,11 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
                 rbias[q] = pair(rb, rb);
                 rgrp[q] = in ? xs.grp[row] : -1;
             }
+            // the thread's share of its rows' sums of P, before and after the rounding
+            f32x2 exact_sum[4];
+            RoundedSum<HITS> round_sum[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) exact_sum[q] = pair(0.f, 0.f);
             // A tile to P, in steps of 64 columns of one 16-row block. P of a step
             // covers logits that the block's threads have read already. Loads and
             // stores of 8 columns each: larger ones tie 32 registers into one
@@ -545,7 +594,10 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
                                     y.x *= ww.x;
                                     y.y *= ww.y;
                                 }
-                                pk[2 * e + q] = bf16x2_bits(y.x, y.y);
+                                const uint32_t bits = bf16x2_bits(y.x, y.y);
+                                pk[2 * e + q] = bits;
+                                exact_sum[2 * k + q] = add2(exact_sum[2 * k + q], pair(y.x, y.y));
+                                round_sum[2 * k + q].add(bits);
                             }
                         }
 #pragma unroll
@@ -579,6 +631,23 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
                     if (t < t1) step_on(t);
             }
             if (!ok) break;
+            {
+                float* sums = p.sums + ((int64_t)(uid + blockIdx.x) * K6_GROUPS + group) * 2 * K6_M + quarter * 32 + (lane >> 2);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 a = unpair(exact_sum[q]);
+                    float exact = a.x + a.y, rounded = round_sum[q].total();
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) {
+                        exact += __shfl_xor_sync(0xffffffffu, exact, o);
+                        rounded += __shfl_xor_sync(0xffffffffu, rounded, o);
+                    }
+                    if ((lane & 3) == 0) {
+                        sums[8 * q] = exact;
+                        sums[K6_M + 8 * q] = rounded;
+                    }
+                }
+            }
             // the product of this segment
             if (!mbar_wait(&ctl->accfull, seg & 1, abort)) { ok = false; break; }
             tc_fence_after();
@@ -618,6 +687,7 @@ __global__ void __launch_bounds__(K6_THREADS, 1)
 // ---------------------------------------------------------------------------
 struct K6Finish {
     const float* part;
+    const float* sums;
     const float *weight, *diag;  // [b]
     const float* common;         // factor of the items' products
     const __nv_bfloat16 *users, *items;
@@ -632,10 +702,13 @@ struct K6Finish {
 // items) and one half of the columns; which parts of the line belong to the
 // tile is found once per block.
 constexpr int K6_FIN_ROWS = 32;
+// The ratio of a row's sums of P before and after the rounding to bf16 lies between these.
+constexpr float K6_SCALE_MIN = 256.f / 257.f, K6_SCALE_MAX = 256.f / 255.f;
 
 template <int TN>
 __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
     __shared__ int first, parts;
+    __shared__ float sums[8][2][K6_FIN_ROWS], scale[K6_FIN_ROWS];
     const K6Line<TN> line(p.b, p.nc);
     pdl_trigger();
     const int per_tile = K6_M / K6_FIN_ROWS;
@@ -657,6 +730,30 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
     const int col0 = half * K6_HALF, cols = p.d - col0 < K6_HALF ? p.d - col0 : K6_HALF;
     const bool failed = *p.err != 0;
     const float common = pass == 1 ? *p.common : 1.f;
+    // the rows' sums of P: a warp per eighth of the parts, then the eight in order
+    {
+        const int r = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        const float* src = p.sums + (int64_t)(uid + first) * K6_GROUPS * 2 * K6_M + row0 % K6_M + r;
+        float exact = 0.f, rounded = 0.f;
+#pragma unroll 4
+        for (int c = warp; c < parts * K6_GROUPS; c += 8) {
+            exact += __ldcg(src + (int64_t)c * 2 * K6_M);
+            rounded += __ldcg(src + (int64_t)c * 2 * K6_M + K6_M);
+        }
+        sums[warp][0][r] = exact;
+        sums[warp][1][r] = rounded;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int q = 1; q < 8; ++q) {
+                exact += sums[q][0][r];
+                rounded += sums[q][1][r];
+            }
+            // no sum: nothing was added
+            scale[r] = rounded != 0.f ? fminf(fmaxf(exact / rounded, K6_SCALE_MIN), K6_SCALE_MAX) : 1.f;
+        }
+        __syncthreads();
+    }
     for (int v = threadIdx.x; v < K6_FIN_ROWS * (cols / 8); v += 256) {
         const int r = v / (cols / 8), c8 = (v - r * (cols / 8)) * 8;
         const int i = row0 + r;
@@ -673,6 +770,8 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
             acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
             acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] *= scale[r];
         const float w = i < p.b ? p.weight[i] : 0.f;
         float out[8];
 #pragma unroll
@@ -759,6 +858,7 @@ SoftmaxGradPlan softmax_grad_plan(int b, int nc, int d, bool item_ids, bool copi
     pl.off_users_c = take(copies ? (size_t)b * d * 2 : 0);
     pl.off_items_c = take(copies ? (size_t)nc * d * 2 : 0);
     pl.off_part = take((size_t)(units + pl.grid) * K6_M * pl.width * sizeof(float));
+    pl.off_sums = take((size_t)(units + pl.grid) * K6_GROUPS * 2 * K6_M * sizeof(float));
     pl.bytes = off;
     return pl;
 }
@@ -837,6 +937,7 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
     p.user = q.user;
     p.weight = q.weight;
     p.part = reinterpret_cast<float*>(ws + pl.off_part);
+    p.sums = reinterpret_cast<float*>(ws + pl.off_sums);
     p.err = q.err;
     p.b = g.b;
     p.nc = g.nc;
@@ -855,6 +956,7 @@ cudaError_t launch_all(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, cudaStre
 
     K6Finish f;
     f.part = p.part;
+    f.sums = p.sums;
     f.weight = q.weight;
     f.diag = q.diag;
     f.common = q.common;

@@ -310,7 +310,7 @@ cudaError_t launch_embedding_grad(const EmbeddingGrad& g, bool by_row, cudaStrea
 struct SoftmaxGradPlan {
     int tile_cols, halves, width, bufs, stages, grid, log2_slots;
     int64_t work;
-    size_t off_err, off_item, off_user, off_weight, off_diag, off_common, off_keys, off_users_c, off_items_c, off_part;
+    size_t off_err, off_item, off_user, off_weight, off_diag, off_common, off_keys, off_users_c, off_items_c, off_part, off_sums;
     size_t bytes;
 };
 // copies: padding is given, so that the products read copies of the rows with

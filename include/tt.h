@@ -576,11 +576,16 @@ TT_API tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64
  *   grad_users_i = w_i / tau (sum_j P_ij v_j - v_i)
  *   grad_items_j = 1 / tau (sum_i w_i P_ij u_i - w_j u_j)   (the last term for j < b)
  *
- * The logits are formed as in the loss; P enters the products rounded to bf16
- * (the diagonal apart, which is added in fp32), the sums are fp32, and the
- * results are rounded to bf16. Rows of padding, users and items, get zero
- * gradients, and what they hold (NaN too) changes nothing. (The loss itself
- * needs finite item rows, padding included.)
+ * The logits are formed as in the loss; P (w_i P_ij for the items, where
+ * grad_loss is given) enters the products rounded to bf16 (the diagonal apart,
+ * which is added in fp32), and each row's product is scaled by the ratio of its
+ * sums of P before and after that rounding: the rounding then leaves at most
+ * 2^-7 of sum_j P_ij |v_j - mean|, so that a component which all rows share
+ * leaves the gradient as the formula says. (Weights of both signs apart: the
+ * scale stays within 1 / (1 +- 2^-8), and up to 2^-7 of sum_i |w_i P_ij u_i| may
+ * be left.) The sums are fp32, and the results are rounded to bf16. Rows of
+ * padding, users and items, get zero gradients, and what they hold (NaN too)
+ * changes nothing. (The loss itself needs finite item rows, padding included.)
  *
  * users, items, dtype, b, nc, d, tau, logq, item_ids, valid
  *             as for tt_inbatch_softmax, and the same values (nc at most 2^30)
