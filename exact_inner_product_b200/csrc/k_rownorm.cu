@@ -302,6 +302,15 @@ __global__ void __launch_bounds__(L > 0 ? K7_THREADS : CH == 8 ? 320 : 512)
     constexpr bool DIVIDE = L > 0 && CH == 4;
     const float inv_d = 1.0f / (float)d;
     auto over_d = [&](float sum) { return DIVIDE ? sum / (float)d : sum * inv_d; };
+    // The mean takes the product's remainder too, which a division would not have:
+    // a row of one number whose sum is exact has that number as its mean, and not one
+    // beside it, which rstd would blow up (12289 at 500 columns: y = -0.3 for 0).
+    auto mean_of = [&](float sum) {
+        const float m = over_d(sum);
+        if (DIVIDE) return m;
+        const float rest = fmaf(-m, (float)d, sum);
+        return rest == rest ? fmaf(rest, inv_d, m) : m;  // an infinite mean stays
+    };
     if (AHEAD) load(g.row);
     for (; g.any(n); g.row += R * g.step) {
         if (!AHEAD) load(g.row);
@@ -321,7 +330,7 @@ __global__ void __launch_bounds__(L > 0 ? K7_THREADS : CH == 8 ? 320 : 512)
         }
         if (AHEAD) load(g.row + R * g.step);
 #pragma unroll
-        for (int r = 0; r < R; ++r) mean[r] = over_d(g.sums(mean[r], 0.f, sm).x);
+        for (int r = 0; r < R; ++r) mean[r] = mean_of(g.sums(mean[r], 0.f, sm).x);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const f32x2 minus = pair(-mean[r], -mean[r]);

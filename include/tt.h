@@ -442,7 +442,9 @@ TT_API tt_status tt_inbatch_softmax_check(const void* workspace, void* stream);
  * d           1 <= d <= TT_MAX_WIDTH, any value (multiples of 8 are fastest)
  * w, bias     device [d] w_dtype (TT_F32 or TT_BF16), 16-byte aligned, either
  *             may be NULL (1 and 0)
- * eps         finite, >= 0 (with 0, a constant row gives 0 * inf = NaN)
+ * eps         finite, >= 0. A row of one number gives x - mean = 0, and with eps
+ *             = 0 then 0 * inf = NaN, if fp32 holds the row's sum exactly; else
+ *             the mean, and x - mean, may be off by a few units in x's last place
  * mean, rstd  device f32 [n], either may be NULL: kept for the gradient
  */
 TT_API tt_status tt_layernorm(const void* x, tt_dtype dtype, int64_t n, int32_t d, const void* w, const void* bias,
