@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(K8_RUN_WARPS * 32)
     __shared__ Open open[K8_RUN_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t chunk = (int64_t)blockIdx.x * K8_RUN_WARPS + warp;
-    pdl_trigger();
+    if (gridDim.x > 1) pdl_trigger();  // k8_join follows; a call's last kernel must not (tt_device.cuh)
     pdl_wait();
     const int64_t i0 = chunk * K8_RUN;
     const int64_t i = i0 + lane;

@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
     __shared__ int first, parts;
     __shared__ float sums[8][2][K6_FIN_ROWS], scale[K6_FIN_ROWS];
     const K6Line<TN> line(p.b, p.nc);
-    pdl_trigger();
+    // no pdl_trigger: the last kernel, and its rows may be the next call's (tt_device.cuh)
     const int per_tile = K6_M / K6_FIN_ROWS;
     const int q = blockIdx.x / per_tile;  // row tile
     const int pass = q < line.ru ? 0 : 1;

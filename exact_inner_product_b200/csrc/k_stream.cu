@@ -112,9 +112,10 @@ __device__ __forceinline__ void append_warp(const PassArgs& a, int q, bool keep,
 // thread scores its first DEFER rows before it waits for that kernel, keeps
 // their keys in registers and filters them once the threshold is known, so
 // the first blocks stream rows while the estimate runs. Reading the rows and
-// the queries before the wait is safe: no kernel that writes them signals its
-// dependents early, so the search's first kernel, and with it every later
-// one, starts only after those writes completed.
+// the queries before the wait is safe: no kernel that writes them (the last ones
+// of the training calls among them) signals its dependents early, so the search's
+// first kernel, and with it every later one, starts only after those writes
+// completed.
 template <typename T, int QB, bool V8, bool PF, int DEFER>
 __global__ void __launch_bounds__(K2_THREADS)
     k2_stream(const PassArgs a) {

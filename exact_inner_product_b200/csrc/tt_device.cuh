@@ -77,6 +77,11 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // kernel writes or reads (the wait returns once that kernel has completed and
 // its writes are visible; without such a kernel it returns at once), and it
 // calls pdl_trigger() to let the next kernel of the stream launch early.
+//
+// A call's last kernel must not trigger if it writes rows or queries: a search
+// that is enqueued next reads its corpus and queries before its wait (k2_stream
+// with DEFER), and that is safe only because its first kernel, and so every later
+// one, starts after the writes of the call before it have completed.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
