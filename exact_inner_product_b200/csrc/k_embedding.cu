@@ -898,7 +898,7 @@ cudaError_t sort_tokens(const GradPlan& p, const void* ids, int64_t m, uint32_t 
         const int grid = bytes == 0 ? 1 : 1 + (int)(fill < 1 ? 1 : fill < sm_count - 1 ? fill : sm_count - 1);
         auto launch = [&](auto kernel, size_t smem) {
             if (smem > 48 * 1024 &&
-                (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess)
+                (e = allow_smem(kernel, smem)) != cudaSuccess)  // the same for every call
                 return e;
             note_launch_begin(TT_KIND_EMBEDDING, s);
             kernel<<<grid, threads, smem, s>>>(static_cast<const ID*>(ids), (int)m, rows, p.passes, p.bits, tok[0],

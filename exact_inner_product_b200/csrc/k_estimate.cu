@@ -95,7 +95,7 @@ cudaError_t launch_estimate(const EstimateArgs& a, cudaStream_t s) {
     if (a.rank < 1 || a.rank > ESTIMATE_MAX_RANK) return cudaErrorInvalidValue;
     if ((int64_t)G * a.rank > K4_SMEM_KEYS || (int64_t)G * a.rank > a.cap) return cudaErrorInvalidValue;
     const size_t smem = sizeof(K4Smem) + (size_t)a.d * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(k2_estimate, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(k2_estimate, sizeof(K4Smem) + TT_MAX_D * sizeof(float));
     if (e != cudaSuccess) return e;
     note_launch_begin(TT_KIND_ESTIMATE, s);
     e = launch_pdl(k2_estimate, dim3((unsigned)G, (unsigned)a.b), dim3(KE_THREADS), smem, s, a);

@@ -173,7 +173,7 @@ int exact_chunks(int64_t n, int k, int cap) {
 cudaError_t launch_exact(const ExactArgs& a, cudaStream_t s, int sm_count) {
     if (a.V == 0 || a.k == 0) return cudaSuccess;
     const size_t smem = sizeof(K4Smem) + (size_t)a.d * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(k4_exact, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(k4_exact, sizeof(K4Smem) + TT_MAX_D * sizeof(float));
     if (e != cudaSuccess) return e;
     // one block per SM at most: a search that needs no repair launches few
     // blocks, each of which returns at once

@@ -986,9 +986,11 @@ cudaError_t ln_launch(const LnArgs& a, bool grad, const RowShape& r) {
     const int own = ALIGNED ? 0 : threads * CH * 32;  // a thread's weights
     const int red = L > 0 ? (ALIGNED ? warps : warps * 32 / (L > 0 ? L : 1)) * L * CH * 32 : 0;
     const int smem = grad ? (red > own ? red : own) : 2 * own;
+    // a block per row has up to 512 threads (320 with eight chunks)
+    constexpr int WIDEST = ALIGNED || L > 0 ? 0 : 2 * (CH == 8 ? 320 : 512) * CH * 32;
     auto raise = [&](auto* kernel) {
-        if (smem <= 48 * 1024) return cudaSuccess;
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const int most = smem > WIDEST ? smem : WIDEST;
+        return most <= 48 * 1024 ? cudaSuccess : allow_smem(kernel, most);
     };
     auto run_grad = [&](auto* kernel) {
         if (const cudaError_t e = raise(kernel); e != cudaSuccess) return e;

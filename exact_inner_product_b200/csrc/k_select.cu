@@ -207,7 +207,7 @@ cudaError_t launch_select_threshold(const uint64_t* keys, uint32_t* count, int c
                                     uint64_t* theta_next, float* thf_next, cudaStream_t s) {
     if (b == 0) return cudaSuccess;
     const int smem = (int)sizeof(K4Smem);
-    cudaFuncSetAttribute(k4_select_threshold, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    allow_smem(k4_select_threshold, smem);
     note_launch_begin(TT_KIND_SELECT, s);
     const cudaError_t e = launch_pdl(k4_select_threshold, dim3(b), dim3(K4_THREADS), smem, s, keys, count, cap, r,
                                      theta_next, thf_next);
@@ -220,7 +220,7 @@ cudaError_t launch_select_final(const uint64_t* keys, uint32_t* count, int cap, 
                                 int32_t* out_ids, float* out_scores, cudaStream_t s) {
     if (b == 0) return cudaSuccess;
     const int smem = (int)sizeof(K4Smem);
-    cudaFuncSetAttribute(k4_select_final, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    allow_smem(k4_select_final, smem);
     note_launch_begin(TT_KIND_SELECT, s);
     const cudaError_t e = launch_pdl(k4_select_final, dim3(b), dim3(K4_THREADS), smem, s, keys, count, cap, k,
                                      theta, thf, flagged, flags, out_ids, out_scores);
@@ -236,7 +236,7 @@ cudaError_t launch_merge(const int32_t* ids, const float* scores, int parts, int
     MergeOffsets id_offset;
     for (int p = 0; p < TT_MAX_PARTS; ++p) id_offset.v[p] = p < parts ? id_offset_host[p] : 0;
     const int smem = (int)sizeof(K4Smem);
-    cudaFuncSetAttribute(k4_merge, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    allow_smem(k4_merge, smem);
     note_launch_begin(TT_KIND_SELECT, s);
     k4_merge<<<b, K4_THREADS, smem, s>>>(ids, scores, parts, b, k_in, id_offset, k_out, scratch, out_ids,
                                          out_scores);

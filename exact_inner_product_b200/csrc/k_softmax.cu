@@ -931,8 +931,7 @@ cudaError_t launch_softmax(const SoftmaxPlan& pl, const CUtensorMap& tm_users, c
     const int smem = 1024 + p.kchunks * K5_USER_CHUNK + p.stages * K5_STAGE_BYTES + (int)sizeof(K5Ctl);
     const int n_units = p.u_tiles * p.chunks;
     const int grid = n_units < sm_count ? n_units : sm_count;
-    e = hits ? cudaFuncSetAttribute(k5_softmax<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)
-             : cudaFuncSetAttribute(k5_softmax<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = allow_smem(hits ? k5_softmax<true> : k5_softmax<false>, K5_SMEM_BUDGET);
     if (e != cudaSuccess) return e;
     note_launch_begin(TT_KIND_SOFTMAX, s);
     if (hits)

@@ -868,7 +868,7 @@ namespace {
 template <int TN, bool HITS>
 cudaError_t launch_products(const SoftmaxGradPlan& pl, const SoftmaxGrad& g, const K6Params& p, cudaStream_t s) {
     const int smem = 1024 + p.kchunks * K6_M * 128 + p.stages * (p.kchunks * TN * 128 + TN * 12) + (int)sizeof(K6Ctl);
-    cudaError_t e = cudaFuncSetAttribute(k6_products<TN, HITS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(k6_products<TN, HITS>, K6_SMEM_BUDGET);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes attr;
     if ((e = cudaFuncGetAttributes(&attr, k6_products<TN, HITS>)) != cudaSuccess) return e;

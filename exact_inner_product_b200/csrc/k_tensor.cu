@@ -473,7 +473,7 @@ cudaError_t launch_tensor_pass(const PassArgs& a, const CUtensorMap& tm_rows,
     const int grid = n_units < sm_count ? n_units : sm_count;
     auto kern = i8 ? (p.kps == 2 ? k3_tensor<true, 2> : k3_tensor<true, 1>)
                    : (p.kps == 2 ? k3_tensor<false, 2> : k3_tensor<false, 1>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(kern, K3_SMEM_BUDGET);
     if (e != cudaSuccess) return e;
     note_launch_begin(TT_KIND_TENSOR, s);
     kern<<<grid, K3_THREADS, smem, s>>>(tm_rows, tm_queries, p);

@@ -572,7 +572,7 @@ cudaError_t launch_variant(const KPParams& base, const CUtensorMap& tm_rows, con
         cfg.blockDim = dim3(KP_THREADS);
         cfg.dynamicSmemBytes = (size_t)smem;
         int max_clusters = 0;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = allow_smem(kern, KP_SMEM_BUDGET);
         if (e != cudaSuccess) return e;
         if (cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg) == cudaSuccess) {
             if (max_clusters > 0 && max_clusters < pairs) pairs = max_clusters;

@@ -53,6 +53,16 @@ bool valid_dtype(int dt);  // TT_F32 or TT_BF16
 tt_status check_device_ptr(const void* p, const char* what);
 int sm_count_current();
 
+// Lets `kernel` be launched with up to `most` bytes of dynamic shared memory. The
+// limit belongs to the kernel and is shared by all host threads, so a kernel whose
+// need depends on the call has one `most` for all calls: a smaller limit set by
+// another thread's call could land between this one's and its launch, which then
+// fails.
+template <typename K>
+cudaError_t allow_smem(K* kernel, size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
 // Launch `kernel` with programmatic stream serialization: it may start while
 // the stream's previous kernel still runs (the kernel then orders its memory
 // accesses with pdl_wait(), see tt_device.cuh).
