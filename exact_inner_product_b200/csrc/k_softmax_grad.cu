@@ -777,9 +777,11 @@ __global__ void __launch_bounds__(256) k6_finish(const K6Finish p) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) out[k] = pass == 0 ? 0.f : acc[k] * common * p.inv_tau;
         if (w != 0.f) {
+            // past L1, and not as read-only data: with padding these are copies that
+            // k6_prepare wrote, maybe when this block was there already
             Raw<__nv_bfloat16, 8> other;
             float x[8];
-            other.load((pass == 0 ? p.items : p.users) + (int64_t)i * p.d + col0 + c8);
+            other.a = __ldcg(reinterpret_cast<const uint4*>((pass == 0 ? p.items : p.users) + (int64_t)i * p.d + col0 + c8));
             other.get(x);
             const float c_ii = p.diag[i];
             if (pass == 0) {

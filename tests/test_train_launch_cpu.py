@@ -34,3 +34,13 @@ def test_a_calls_last_kernel_does_not_signal_early():
     # the runs are the last kernel where one block holds them all
     runs = _body("k_embedding.cu", "k8_runs")
     assert runs.count("pdl_trigger") == 1 and "if (gridDim.x > 1) pdl_trigger();" in runs
+
+
+def test_what_the_call_wrote_is_not_read_as_read_only_data():
+    """__ldg is for data that nothing writes while the kernel lives, and these kernels may be there before
+    an earlier one of the call has written what they read."""
+    for source, kernels in {"k_softmax_grad.cu": ["k6_finish"], "k_embedding.cu": ["k8_scan", "k8_heads", "k8_join"],
+                            "k_rownorm.cu": ["k7_columns"]}.items():
+        for kernel in kernels:
+            body = _body(source, kernel)
+            assert "__ldg(" not in body and ".load(" not in body, kernel
