@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
     pdl_trigger();
     if (threadIdx.x == 0) valid_rows = 0;
     __syncthreads();
+    pdl_wait();  // the empty table, the call's inputs, and whoever used the workspace before
     if (p.valid != nullptr && p.grad_mean != nullptr) {  // every block counts all rows
         int n = 0;
         const bool words = (reinterpret_cast<uintptr_t>(p.valid) & 15) == 0;
@@ -232,7 +233,6 @@ __global__ void __launch_bounds__(K6_PREP_THREADS) k6_prepare(const K6Prep p) {
     // the weight of every valid row, where there is no gradient per row
     const int count = p.valid != nullptr ? valid_rows : p.b;
     const float mean_w = p.grad_mean != nullptr && count > 0 ? *p.grad_mean / (float)count : 0.f;
-    pdl_wait();  // the empty table, and whoever used the workspace before
     if (tid == 0) *p.err = 0;
     if (tid == 0) *p.common = p.grad_loss != nullptr ? 1.f : mean_w;
     // past the end, to whole tiles: columns without a share

@@ -44,3 +44,14 @@ def test_what_the_call_wrote_is_not_read_as_read_only_data():
         for kernel in kernels:
             body = _body(source, kernel)
             assert "__ldg(" not in body and ".load(" not in body, kernel
+
+
+def test_memory_is_touched_after_the_wait():
+    """Kernels that may start early: nothing of the call's arguments is read or written before the wait."""
+    for source, kernels in {"k_softmax_grad.cu": ["k6_prepare", "k6_products", "k6_finish"], "k_rownorm.cu": ["k7_columns"],
+                            "k_embedding.cu": ["k8_count", "k8_scan", "k8_scatter", "k8_heads", "k8_runs", "k8_join"]}.items():
+        for kernel in kernels:
+            before = _body(source, kernel).split("pdl_wait();")[0]
+            assert len(before) < len(_body(source, kernel)), kernel
+            touched = re.search(r"__ldc?g\(|\*\s*[pa]\.\w+|\b[pa]\.\w+(\.\w+)?\s*\[|load_token", before)
+            assert not touched, (kernel, touched.group(0))
