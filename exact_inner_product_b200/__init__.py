@@ -288,10 +288,11 @@ def tt_score_topk(index: Index, queries: torch.Tensor, k: int, tau: float = 1.0,
     if d != index.d:
         raise ValueError(f"queries have d={d}, index has d={index.d}")
     dev = queries.device
-    if out_ids is None:
-        out_ids = torch.empty((b, k), dtype=torch.int32, device=dev)
-    if out_scores is None:
-        out_scores = torch.empty((b, k), dtype=torch.float32, device=dev)
+    with _on(stream):
+        if out_ids is None:
+            out_ids = torch.empty((b, k), dtype=torch.int32, device=dev)
+        if out_scores is None:
+            out_scores = torch.empty((b, k), dtype=torch.float32, device=dev)
     if exclude is not None and (exclude.dtype not in (torch.int32,) or not exclude.is_contiguous()):
         raise TypeError("exclude must be a contiguous int32 tensor of packed bits")
     if options:
@@ -323,10 +324,11 @@ def tt_score_topk_noalloc(rows: torch.Tensor, queries: torch.Tensor, k: int, tau
     if queries.shape[1] != d:
         raise ValueError(f"queries have d={queries.shape[1]}, rows have d={d}")
     dev = queries.device
-    if out_ids is None:
-        out_ids = torch.empty((b, k), dtype=torch.int32, device=dev)
-    if out_scores is None:
-        out_scores = torch.empty((b, k), dtype=torch.float32, device=dev)
+    with _on(stream):
+        if out_ids is None:
+            out_ids = torch.empty((b, k), dtype=torch.int32, device=dev)
+        if out_scores is None:
+            out_scores = torch.empty((b, k), dtype=torch.float32, device=dev)
     for name, t, dt in (("out_ids", out_ids, torch.int32), ("out_scores", out_scores, torch.float32)):
         if t.dtype != dt or tuple(t.shape) != (b, k) or not t.is_contiguous() or t.device != dev:
             raise ValueError(f"{name} must be a contiguous {dt} tensor of shape ({b}, {k}) on {dev}")
@@ -397,10 +399,11 @@ def tt_merge_topk(ids: torch.Tensor, scores: torch.Tensor, id_offsets, k_out: in
     if len(id_offsets) != parts:
         raise ValueError("one offset per part")
     dev = ids.device
-    if out_ids is None:
-        out_ids = torch.empty((b, k_out), dtype=torch.int32, device=dev)
-    if out_scores is None:
-        out_scores = torch.empty((b, k_out), dtype=torch.float32, device=dev)
+    with _on(stream):
+        if out_ids is None:
+            out_ids = torch.empty((b, k_out), dtype=torch.int32, device=dev)
+        if out_scores is None:
+            out_scores = torch.empty((b, k_out), dtype=torch.float32, device=dev)
     _check(_lib.tt_merge_topk(_ptr(ids), _ptr(scores), parts, b, k_in, offs, int(k_out), _ptr(out_ids),
                               _ptr(out_scores), _stream(stream)), "tt_merge_topk")
     return out_ids, out_scores
@@ -442,12 +445,13 @@ def tt_inbatch_softmax(users: torch.Tensor, items: torch.Tensor, tau: float = 1.
         if valid.dtype != torch.uint8 or not valid.is_contiguous() or valid.numel() != nc:
             raise TypeError("valid must be a contiguous bool or uint8 tensor of nc elements")
     need = tt_inbatch_softmax_workspace(b, nc, d, item_ids is not None)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=users.device)
-    if out is None:
-        out = (torch.empty(b, dtype=torch.float32, device=users.device),
-               torch.empty(b, dtype=torch.float32, device=users.device),
-               torch.empty((), dtype=torch.float32, device=users.device))
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=users.device)
+        if out is None:
+            out = (torch.empty(b, dtype=torch.float32, device=users.device),
+                   torch.empty(b, dtype=torch.float32, device=users.device),
+                   torch.empty((), dtype=torch.float32, device=users.device))
     lse, loss, mean = out
     _check(_lib.tt_inbatch_softmax(_ptr(users), _ptr(items), _dtype(users), b, nc, d, float(tau), _ptr(logq), _ptr(item_ids),
                                    _ptr(valid), _ptr(lse), _ptr(loss), _ptr(mean), _ptr(workspace),
@@ -849,8 +853,9 @@ def tt_score_topk_ranges(index: Index, queries: torch.Tensor, k: int, ranges, ta
     b = queries.shape[0]
     R = len(ranges)
     flat = (_i64 * (2 * max(1, R)))(*[int(v) for rng in ranges for v in rng])
-    out_ids = torch.empty((R, b, k), dtype=torch.int32, device=queries.device)
-    out_scores = torch.empty((R, b, k), dtype=torch.float32, device=queries.device)
+    with _on(stream):
+        out_ids = torch.empty((R, b, k), dtype=torch.int32, device=queries.device)
+        out_scores = torch.empty((R, b, k), dtype=torch.float32, device=queries.device)
     _check(_lib.tt_score_topk_ranges(index.handle, _ptr(queries), _dtype(queries), b, _ptr(exclude), float(tau),
                                      int(k), R, flat, _ptr(out_ids), _ptr(out_scores), _stream(stream)),
            "tt_score_topk_ranges")
@@ -868,8 +873,9 @@ def tt_score_topk_types(index: Index, queries: torch.Tensor, k: int, types: torc
     b = queries.shape[0]
     T = len(set_types)
     st_arr = (_i32 * max(1, T))(*[int(t) for t in set_types])
-    out_ids = torch.empty((T, b, k), dtype=torch.int32, device=queries.device)
-    out_scores = torch.empty((T, b, k), dtype=torch.float32, device=queries.device)
+    with _on(stream):
+        out_ids = torch.empty((T, b, k), dtype=torch.int32, device=queries.device)
+        out_scores = torch.empty((T, b, k), dtype=torch.float32, device=queries.device)
     _check(_lib.tt_score_topk_types(index.handle, _ptr(queries), _dtype(queries), b, _ptr(exclude), float(tau),
                                     int(k), _ptr(types), T, st_arr, _ptr(out_ids), _ptr(out_scores),
                                     _stream(stream)), "tt_score_topk_types")
