@@ -65,7 +65,10 @@ namespace tt {
 // ---------------------------------------------------------------------------
 static thread_local char g_last_error[256] = {0};
 
+// A failed launch or copy: the message is kept, and the runtime's last error
+// cleared, so that a later call does not report this one's.
 tt_status cuda_fail(cudaError_t e, const char* what) {
+    cudaGetLastError();
     snprintf(g_last_error, sizeof g_last_error, "%s: %s", what, cudaGetErrorString(e));
     return e == cudaErrorMemoryAllocation ? TT_ERR_NO_MEMORY : TT_ERR_CUDA;
 }

@@ -13,21 +13,14 @@
 #include "../../include/tt.h"
 #include "tt_internal.h"
 
-#define TT_CUDA(call, what)                                 \
-    do {                                                    \
-        const cudaError_t _e = (call);                      \
-        if (_e != cudaSuccess) return call_failed(_e, what); \
+#define TT_CUDA(call, what)                                \
+    do {                                                   \
+        const cudaError_t _e = (call);                     \
+        if (_e != cudaSuccess) return cuda_fail(_e, what); \
     } while (0)
 
 namespace tt {
 namespace {
-
-// A failed launch or copy: the message is kept, and the runtime's last error
-// cleared, so that a later call does not report this one's.
-tt_status call_failed(cudaError_t e, const char* what) {
-    cudaGetLastError();
-    return cuda_fail(e, what);
-}
 
 size_t elem_bytes(int dtype) { return dtype == TT_F32 ? 4 : 2; }
 
@@ -192,7 +185,7 @@ tt_status clip(const ClipList& l, bool scale, float max_norm, float* norm, void*
     if ((st = check_device_ptr(workspace, "workspace")) != TT_OK) return st;
     const cudaError_t e = launch_clip(l, scale, max_norm, norm, static_cast<double*>(workspace),
                                       static_cast<cudaStream_t>(stream), sms);
-    return e == cudaSuccess ? TT_OK : call_failed(e, "gradient norm");
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "gradient norm");
 }
 
 tt_status check_embedding(int64_t rows, int32_t d, int32_t id_bytes, int64_t m, float scale) {
@@ -225,7 +218,7 @@ tt_status embedding_grad(const EmbeddingGrad& g, bool by_row, size_t workspace_b
     b.out(g.workspace, need, "workspace");
     if ((st = b.check()) != TT_OK) return st;
     const cudaError_t e = launch_embedding_grad(g, by_row, static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : call_failed(e, "embedding gradient");
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "embedding gradient");
 }
 
 }  // namespace
@@ -257,7 +250,7 @@ tt_status tt_layernorm(const void* x, tt_dtype dtype, int64_t n, int32_t d, cons
     if ((st = b.check()) != TT_OK) return st;
     const cudaError_t e = launch_layernorm(x, dtype, n, d, w, bias, w_dtype, eps, y, mean, rstd,
                                            static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : call_failed(e, "layer norm");
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "layer norm");
 }
 
 tt_status tt_layernorm_grad_workspace(int64_t n, int32_t d, size_t* bytes) {
@@ -296,7 +289,7 @@ tt_status tt_layernorm_grad(const void* grad_y, const void* x, tt_dtype dtype, i
     const cudaError_t e =
         launch_layernorm_grad(grad_y, x, dtype, n, d, w, w_dtype, mean, rstd, grad_x, grad_w, grad_bias,
                               static_cast<float*>(workspace), static_cast<cudaStream_t>(stream), sms);
-    return e == cudaSuccess ? TT_OK : call_failed(e, "layer norm gradient");
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "layer norm gradient");
 }
 
 tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x, tt_dtype dtype, int64_t n, int32_t d,
@@ -316,7 +309,7 @@ tt_status tt_normalize_grad(const void* grad_y, tt_dtype g_dtype, const void* x,
     if (st != TT_OK) return st;
     const cudaError_t e = launch_normalize_grad(grad_y, g_dtype, x, dtype, n, d, grad_x,
                                                 static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : call_failed(e, "normalisation gradient");
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "normalisation gradient");
 }
 
 tt_status tt_clip_grad_norm_workspace(int32_t count, const int64_t* n, const int32_t* dtypes, size_t* bytes) {
@@ -355,7 +348,7 @@ tt_status tt_embedding(const void* table, tt_dtype table_dtype, int64_t rows, in
     if ((st = b.check()) != TT_OK) return st;
     const cudaError_t e = launch_embedding(table, table_dtype, rows, d, ids, id_bytes, m, scale, out, out_dtype,
                                            static_cast<cudaStream_t>(stream), sm_count_current());
-    return e == cudaSuccess ? TT_OK : call_failed(e, "embedding lookup");
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "embedding lookup");
 }
 
 tt_status tt_embedding_grad_workspace(int64_t m, int64_t rows, int32_t d, size_t* bytes) {
@@ -464,7 +457,7 @@ tt_status tt_inbatch_softmax_grad(const void* users, const void* items, tt_dtype
     g.grad_items = grad_items;
     g.workspace = workspace;
     const cudaError_t e = launch_softmax_grad(pl, g, s, sms);
-    return e == cudaSuccess ? TT_OK : call_failed(e, "in-batch softmax gradient");
+    return e == cudaSuccess ? TT_OK : cuda_fail(e, "in-batch softmax gradient");
 }
 
 }  // extern "C"
