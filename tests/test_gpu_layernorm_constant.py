@@ -33,3 +33,17 @@ def test_constant_rows(d, dtype):
     assert bool(((rstd.double() * 1e-5 ** 0.5 - 1).abs() <= 5 * 2.0 ** -24).all())
     y, mean, rstd = tt.tt_layernorm(x, eps=0.0)
     assert bool(torch.isnan(y).all()) and bool(torch.isinf(rstd).all())
+
+
+@pytest.mark.parametrize("d", [7, 56, 500, 777, 1128, 2401])
+def test_infinite_and_huge_means(d):
+    """The mean of a row with an infinity is that infinity, of one with NaN NaN; a sum near the largest
+    fp32 number keeps its mean."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    x = torch.ones((4, d), device="cuda")
+    x[0, d // 2], x[1, 0], x[2, d - 1] = float("inf"), float("-inf"), float("nan")
+    x[3] = 2.0 ** 127 / 2 ** (d - 1).bit_length()  # every partial sum is exact
+    _, mean, _ = tt.tt_layernorm(x)
+    assert float(mean[0]) == float("inf") and float(mean[1]) == float("-inf") and bool(torch.isnan(mean[2]))
+    assert float(mean[3]) == float(x[3, 0])
