@@ -258,10 +258,12 @@ __global__ void __launch_bounds__(L > 0 ? K7_THREADS : CH == 8 ? 320 : 512)
     k7_layernorm(const T* __restrict__ x, const TW* __restrict__ w, const TW* __restrict__ bias, T* __restrict__ y,
                  float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t n, int d, float eps) {
     constexpr int R = forward_rows<L, CH, ALIGNED>();
-    // The next row's loads ahead pay where a block has a row, and for rows whose
-    // first and last chunks need work before the sums (400000 x 201 bf16 177 against
-    // 144 us); with a warp per whole row the other warps' loads do as well (200003 x
-    // 512 bf16: 158 us ahead, 148 not), and so they do with four chunks.
+    // The next row's loads ahead pay where a block has a row (30000 x 2400 bf16: 98 us
+    // ahead, 113 not), and for rows whose first and last chunks need work before the
+    // sums (400000 x 201 bf16: 121 against 157); with a warp per whole row the other
+    // warps' loads do as well in most cases (200003 x 512 fp32: 140 us ahead, 136 not;
+    // 65536 x 1000 bf16: 70 against 63; but 200003 x 512 bf16: 89 against 99), and so
+    // they do with four chunks.
     constexpr bool AHEAD = L == 0 ? ALIGNED : !ALIGNED && CH <= 2;
     __shared__ float2 sm[2][32];
     extern __shared__ float4 places[];

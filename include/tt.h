@@ -599,6 +599,10 @@ TT_API tt_status tt_embedding_grad_rows(const void* ids, int32_t id_bytes, int64
  * grad_items  device bf16 [nc, d]
  * workspace   tt_inbatch_softmax_grad_workspace bytes
  *
+ * A learned temperature: the gradient with respect to tau is
+ * -1 / tau sum_i <users_i, grad_users_i> (the logits depend on tau through
+ * users / tau alone), with the bf16 rounding of grad_users.
+ *
  * A device-side timeout is reported as for tt_inbatch_softmax: NaN in every
  * output, and TT_ERR_TIMEOUT from tt_inbatch_softmax_check(workspace).
  */
